@@ -92,8 +92,12 @@ enum {
     MX_ERR_ALLOC = -8,      /* split-K workspace allocation failed            */
     MX_ERR_LAUNCH = -9,     /* a kernel launch failed                         */
     MX_ERR_IN_DTYPE = -10,  /* in_dtype is not MX_IN_FP32 / MX_IN_BF16       */
-    MX_ERR_SCRATCH = -11    /* mx_gemm_noalloc: the problem's split-K workspace
+    MX_ERR_SCRATCH = -11,   /* mx_gemm_noalloc: the problem's split-K workspace
                                exceeds MX_NOALLOC_SCRATCH_BYTES               */
+    MX_ERR_ROW_SHAPE = -12, /* a size or pitch a row, routing or epilogue
+                               operator does not take                         */
+    MX_ERR_WORKSPACE = -13, /* the caller's workspace is too small             */
+    MX_ERR_ACT = -14        /* act is not an MX_ACT_* code                     */
 };
 
 /* Input element types of mx_quantize. */
@@ -447,6 +451,175 @@ int mx_mfma_ceiling(int fmt, int64_t steps, int random_data, float *out, void *s
  * MX_ERR_SHAPE, MX_ERR_ALIGN, a device error or MX_ERR_LAUNCH.
  */
 int mx_hbm_read_ceiling(const void *src, int64_t bytes, uint32_t *out, void *stream);
+
+/*
+ * -------------------------------------------------------------------------
+ * The operators between two products of a transformer block: row operators
+ * (norm, gated activation) whose outputs are MX operands, expert routing
+ * around mx_gemm_grouped, and products with a fused epilogue.
+ *
+ * Common to them:
+ *   - dtype is MX_IN_FP32 or MX_IN_BF16, the type of the rows they read and
+ *     write; sums, statistics and weights are FP32, and each output is
+ *     rounded once (to nearest even), from FP32;
+ *   - ld* arguments are row pitches in elements (in bytes for
+ *     mx_moe_gather), at least the row's length; outputs are dense;
+ *   - rows of floating values start 16-byte aligned (pointer and pitch);
+ *   - zero rows or tokens are allowed: nothing is launched and no pointer is
+ *     looked at (a dW or group_rows that is asked for is still written);
+ *   - errors, asynchrony and determinism are as for mx_gemm.  An output
+ *     overlaps no input unless it says otherwise.  They allocate nothing and
+ *     can be captured in a graph; where a workspace is needed it is the
+ *     caller's, used on `stream` until the call's work is done there.
+ */
+
+/* Longest row of a row operator. */
+#define MX_ROW_MAX_WIDTH 65536
+
+/*
+ * Residual addition, root-mean-square norm and MX quantization in one pass:
+ *   H = X + R (rounded to dtype),  rstd = 1 / sqrt(mean_j H_j^2 + eps),
+ *   Y_j = H_j * rstd * W_j,        (Q, Q_scale) = MX(Y), from the unrounded Y.
+ *   fmt        any MX_FMT_* code (not looked at without Q)
+ *   w_dtype    MX_IN_FP32 or MX_IN_BF16, the type of W (width values)
+ *   width      a multiple of 32, at most MX_ROW_MAX_WIDTH
+ *   R          NULL: no residual, H = X
+ *   H          rows x width, written only with R (may be X or R itself when
+ *              that is dense)
+ *   Y          rows x width in dtype, or NULL
+ *   Q, Q_scale mx_quantize's layout (Q 8-byte aligned), or NULL; Y and Q may
+ *              not both be NULL
+ *   rstd       rows floats for mx_rmsnorm_backward, or NULL
+ *   eps        at least 0
+ * A row with a NaN or an infinity gives NaNs in Y and blocks of scale 255
+ * with zero codes, as mx_quantize does for such blocks.
+ */
+int mx_rmsnorm_quantize(int fmt, int dtype, int w_dtype, int64_t rows, int64_t width,
+                        const void *X, int64_t ldx, const void *R, int64_t ldr, const void *W,
+                        float eps, void *H, void *Y, void *Q, void *Q_scale, float *rstd,
+                        void *stream);
+
+/*
+ * Gradient of mx_rmsnorm_quantize; the MX rounding passes gradients through
+ * unchanged.  With xhat = H * rstd:
+ *   dX = rstd * (dY * W - xhat * mean_j(dY * W * xhat)) + dH
+ *   dW = sum over rows of dY * xhat   (FP32; NULL: not wanted)
+ * dX, rows x width in dtype, is the gradient of X and of R alike.  dH (or
+ * NULL) is the gradient that reaches H from its other uses.
+ *   workspace  mx_rmsnorm_backward_workspace(rows, width) bytes, 16-byte
+ *              aligned; only used for dW
+ */
+int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t width);
+int mx_rmsnorm_backward(int dtype, int w_dtype, int64_t rows, int64_t width, const void *dY,
+                        int64_t lddy, const void *H, int64_t ldh, const float *rstd,
+                        const void *W, const void *dH, int64_t lddh, void *dX, float *dW,
+                        void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Gated activation and MX quantization: GU holds rows of 2 * width values,
+ * gate then up (the output of a fused gate/up product), and
+ *   (Q, Q_scale) = MX(gate * sigmoid(gate) * up).
+ * width as for mx_rmsnorm_quantize; ld >= 2 * width.
+ */
+int mx_swiglu_quantize(int fmt, int dtype, int64_t rows, int64_t width, const void *GU,
+                       int64_t ld, void *Q, void *Q_scale, void *stream);
+
+/*
+ * Its gradient (the MX rounding passes through): with s = sigmoid(gate),
+ *   d_up = dY * gate * s,  d_gate = dY * up * s * (1 + gate * (1 - s)),
+ * written as dense rows of 2 * width values, d_gate then d_up.  dGU may be GU
+ * itself when that is dense.
+ */
+int mx_swiglu_backward(int dtype, int64_t rows, int64_t width, const void *dY, int64_t lddy,
+                       const void *GU, int64_t ld, void *dGU, void *stream);
+
+/* Most choices per token. */
+#define MX_MOE_MAX_TOP 64
+
+/*
+ * Sorts tokens by expert: ids is tokens x top (dense; id_bytes 4 or 8 for
+ * 32- or 64-bit signed integers), the experts each token goes to.  The sort
+ * is stable in the order of ids.
+ *   group_rows device array of `experts` counts: the rows of each expert
+ *              (what mx_gemm_grouped takes, once copied to the host)
+ *   row_of     tokens x top: the row of each (token, choice) in expert order.
+ *              An id outside 0 .. experts - 1 (a padding token, a dropped
+ *              choice) is no expert: its pair comes after all experts', at
+ *              some row r, and row_of holds -1 - r.
+ *   experts    1 .. MX_MAX_GROUPS; tokens * top at most MX_MAX_DIM
+ *   workspace  mx_moe_sort_workspace(tokens, top, experts) bytes (may be 0),
+ *              4-byte aligned
+ */
+int64_t mx_moe_sort_workspace(int64_t tokens, int64_t top, int64_t experts);
+int mx_moe_sort(int id_bytes, int64_t tokens, int64_t top, int64_t experts, const void *ids,
+                int64_t *group_rows, int32_t *row_of, void *workspace, int64_t workspace_bytes,
+                void *stream);
+
+/*
+ * Copies token rows into expert order: row t of X (row_bytes bytes, pitch
+ * ldx bytes) goes to row row_of[t][j] of XS for every choice j, and likewise
+ * its scale_bytes of scales from X_scale to XS_scale (X_scale NULL: none, as
+ * for BF16 rows).  XS and XS_scale have tokens * top dense rows; rows of
+ * pairs without an expert, which come last, are zeros.  Any byte layout and
+ * alignment is taken; 16-byte aligned rows are fastest.  Its gradient is
+ * mx_moe_combine without weights.
+ */
+int mx_moe_gather(int64_t tokens, int64_t top, const int32_t *row_of, const void *X,
+                  int64_t row_bytes, int64_t ldx, const void *X_scale, int64_t scale_bytes,
+                  int64_t lds, void *XS, void *XS_scale, void *stream);
+
+/*
+ * out[t] = R[t] + sum over choices j, in order, of weights[t][j] *
+ * Y[row_of[t][j]], skipping pairs without an expert (nothing of theirs is
+ * read).  A token with none gets R[t], or zeros.
+ *   width      the rows' length, a multiple of 8
+ *   Y          y_rows x width; rows at or past y_rows count as no expert
+ *   weights    tokens x top floats, or NULL: all 1
+ *   R          tokens x width, or NULL: nothing is added
+ *   out        tokens x width (may be R itself when that is dense)
+ */
+int mx_moe_combine(int dtype, int64_t tokens, int64_t top, int64_t width, const int32_t *row_of,
+                   const void *Y, int64_t y_rows, int64_t ldy, const float *weights,
+                   const void *R, int64_t ldr, void *out, void *stream);
+
+/*
+ * Its gradient (R's is dOut itself):
+ *   dY[row_of[t][j]] = weights[t][j] * dOut[t], zeros in the rows of pairs
+ *   without an expert (y_rows, at most tokens * top, covers the rows that are
+ *   wanted); dweights[t][j] = sum over columns of dOut[t] * Y[row_of[t][j]],
+ *   0 without an expert.
+ */
+int mx_moe_combine_backward(int dtype, int64_t tokens, int64_t top, int64_t width,
+                            const int32_t *row_of, const void *dOut, int64_t lddo,
+                            const void *Y, int64_t y_rows, int64_t ldy, const float *weights,
+                            void *dY, float *dweights, void *stream);
+
+/* Activations of a fused epilogue: none, max(x, 0), x * sigmoid(x), and GELU
+ * by erf or by its tanh form. */
+enum { MX_ACT_NONE = 0, MX_ACT_RELU = 1, MX_ACT_SILU = 2, MX_ACT_GELU = 3, MX_ACT_GELU_TANH = 4 };
+
+/*
+ * C = residual + act(A * B^T + bias): mx_gemm_mixed (its plan's choice) with
+ * bias, activation and residual applied to the FP32 sums before C's one
+ * rounding.
+ *   fmt_a,
+ *   fmt_b      E2M1 with E2M1, E4M3 with E4M3, or E4M3 with E2M1;
+ *              MX_ERR_FORMAT otherwise
+ *   bias       N values in bias_dtype (MX_IN_FP32 or MX_IN_BF16), or NULL
+ *   act        MX_ACT_*
+ *   residual   M x N in C's type with pitch ldr, 16-byte aligned, or NULL;
+ *              may be C itself (with ldr == N)
+ * Everything else as for mx_gemm.
+ */
+int mx_gemm_fused(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, const void *A,
+                  const void *A_scale, const void *B, const void *B_scale, const void *bias,
+                  int bias_dtype, int act, const void *residual, int64_t ldr, void *C,
+                  int out_dtype, void *stream);
+
+/* The same on mx_gemm_bf16. */
+int mx_gemm_bf16_fused(int64_t M, int64_t N, int64_t K, const void *A, const void *B,
+                       const void *bias, int bias_dtype, int act, const void *residual,
+                       int64_t ldr, void *C, int out_dtype, void *stream);
 
 #ifdef __cplusplus
 }

@@ -28,6 +28,10 @@ multiplies consecutive row groups of a by their own weights: b is
 
 is the dense BF16 GEMM on the same tile kernels: a (M, K) and b (N, K)
 bfloat16, no scales, K a multiple of 16.
+
+The operators between two products of a transformer block (norm and gated
+activation with MX outputs, expert routing, products with a fused epilogue)
+are in block.py and re-exported here.
 """
 import ctypes
 import os
@@ -60,13 +64,16 @@ MX_ERR_ALLOC = -8
 MX_ERR_LAUNCH = -9
 MX_ERR_IN_DTYPE = -10
 MX_ERR_SCRATCH = -11
+MX_ERR_ROW_SHAPE = -12
+MX_ERR_WORKSPACE = -13
+MX_ERR_ACT = -14
 NOALLOC_SCRATCH_BYTES = 32 << 20   # mx_gemm_noalloc's fixed split-K scratch per device
 
 IN_FP32 = 1
 IN_BF16 = 2
 
 _VALUE_ERRORS = (MX_ERR_FORMAT, MX_ERR_OUT_DTYPE, MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN,
-                 MX_ERR_IN_DTYPE, MX_ERR_SCRATCH)
+                 MX_ERR_IN_DTYPE, MX_ERR_SCRATCH, MX_ERR_ROW_SHAPE, MX_ERR_WORKSPACE, MX_ERR_ACT)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxgemm.so")
 _lib = None
@@ -144,6 +151,7 @@ def lib():
     L.mx_mfma_ceiling.argtypes = [ctypes.c_int, i64, ctypes.c_int, vp, vp]
     L.mx_hbm_read_ceiling.restype = ctypes.c_int
     L.mx_hbm_read_ceiling.argtypes = [vp, i64, vp, vp]
+    block.declare(L)
     _lib = L
     return L
 
@@ -570,3 +578,11 @@ def mx_gemm_grouped_bf16(a, b, group_rows, out_dtype=None, out=None, stream=None
     if rc != MX_OK:
         _raise(rc)
     return out
+
+
+from . import block  # noqa: E402  (uses the names above)
+from .block import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU,  # noqa: E402,F401
+                    MOE_MAX_TOP, ROW_MAX_WIDTH, MoePlan, NormOut, mx_gemm_bf16_fused,
+                    mx_gemm_fused, mx_moe_combine, mx_moe_combine_backward, mx_moe_gather,
+                    mx_moe_sort, mx_rmsnorm_backward, mx_rmsnorm_quantize, mx_swiglu_backward,
+                    mx_swiglu_quantize)

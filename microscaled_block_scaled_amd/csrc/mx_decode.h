@@ -130,11 +130,11 @@ template <int R> __device__ __forceinline__ int decode_swz(int r)
     return R == 256 ? (r & 15) : swz_row<R>(r);
 }
 
-template <int FA, int FB, int OUT, int WA>
-__global__ void __launch_bounds__(kDecodeWaves * 64)
-decode_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
-              const uint8_t *__restrict__ B, const uint8_t *__restrict__ Bs, void *__restrict__ C,
-              int M, int N, int K)
+template <int FA, int FB, int OUT, int WA, typename EP>
+__device__ __forceinline__ void
+decode_body(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
+            const uint8_t *__restrict__ B, const uint8_t *__restrict__ Bs, void *C, int M, int N,
+            int K, const EP &ep)
 {
     using SL = slab<FA, FB>;
     using G = decode_geo<FA, FB, WA>;
@@ -336,6 +336,7 @@ decode_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
             float v = *(const float *)(smem + from[0] + at);
 #pragma unroll
             for (int w = 1; w < kDecodeWaves; ++w) v += *(const float *)(smem + from[w] + at);
+            if constexpr (EP::fused) v = epilogue_at<OUT>(ep, v, m, n0 + c);
             if constexpr (OUT == OF32) ((float *)C)[(int64_t)m * N + n0 + c] = v;
             else ((uint16_t *)C)[(int64_t)m * N + n0 + c] = f32_to_bf16(v);
         }
@@ -389,6 +390,15 @@ decode_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
         for (int gi = 0; gi < ng; ++gi) add_and_store(gi);
     }
     wait_vm0();                                      // the copies past the last group
+}
+
+template <int FA, int FB, int OUT, int WA>
+__global__ void __launch_bounds__(kDecodeWaves * 64)
+decode_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
+              const uint8_t *__restrict__ B, const uint8_t *__restrict__ Bs, void *__restrict__ C,
+              int M, int N, int K)
+{
+    decode_body<FA, FB, OUT, WA>(A, As, B, Bs, C, M, N, K, NoEpilogue{});
 }
 
 }  // namespace mx

@@ -246,6 +246,18 @@ struct NoGroups {
     static constexpr bool grouped = false;
 };
 
+// A GEMM without a fused epilogue writes its sums as they are (the fused one
+// is struct Epilogue of mx_epilogue.h).
+struct NoEpilogue {
+    static constexpr bool fused = false;
+};
+template <typename EP> __device__ float bias_at(const EP &ep, int n);
+template <int OUT, typename EP>
+__device__ float epilogue_at(const EP &ep, float v, int64_t m, int n);
+template <int OUT, int WTN, int PITCH, typename EP>
+__device__ void fused_band(const EP &ep, uint8_t *stage, void *C, int row0, int col0, int M,
+                           int N, int lane);
+
 // Compile-time loop: f(std::integral_constant<int, I>) for I = 0 .. N-1.
 template <typename F, int... I>
 __device__ __forceinline__ void static_for_impl(F &&f, std::integer_sequence<int, I...>)
@@ -288,12 +300,13 @@ __device__ __forceinline__ void static_for(F &&f)
 // swizzle is applied on the global side, since each lane's LDS slot is fixed
 // by its lane id.  The main loop is one basic block (no data-dependent
 // branches), so the compiler keeps the MFMAs where they are written.
-template <int FA, int FB, int OUT, int BM, int BN, int WGM, int WGN, int S, typename GT = NoGroups>
+template <int FA, int FB, int OUT, int BM, int BN, int WGM, int WGN, int S, typename GT = NoGroups,
+          typename EP = NoEpilogue>
 __global__ void __launch_bounds__(WGM * WGN * 64)
 tile_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
             const uint8_t *__restrict__ B, const uint8_t *__restrict__ Bs,
             void *__restrict__ C, int M, int N, int K, int tiles_m, int tiles_n, int gm,
-            int kchunk, int64_t cplane, GT groups = GT{})
+            int kchunk, int64_t cplane, GT groups = GT{}, EP ep = EP{})
 {
     constexpr int NW = WGM * WGN;
     constexpr int WTM = BM / WGM, WTN = BN / WGN;
@@ -320,7 +333,9 @@ tile_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
     constexpr int CPS = SCALED ? (NSI + NW - 1) / NW : 0;  // scale copies per wave per period
     constexpr int NCOPY = CPA + CPB;
     // The epilogue reuses the LDS to stage output bands (see below).
-    typedef typename std::conditional<OUT == OF32, float, uint16_t>::type otype;
+    // A fused epilogue needs the unrounded sums there.
+    constexpr bool FUSED = EP::fused;
+    typedef typename std::conditional<OUT == OF32 || FUSED, float, uint16_t>::type otype;
     constexpr int OS = sizeof(otype);
     constexpr int PITCH = WTN * OS + 16;                   // staging row pitch, bytes
     // (+16: a half-period read of the last row of a short, shifted last
@@ -787,6 +802,11 @@ tile_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
     const bool vec_ok = ((int64_t)N * OS) % 16 == 0;
     otype *const Cp = (otype *)C + (int64_t)slice * cplane;
     const int col0 = n0 + wn * WTN;
+    [[maybe_unused]] float bias[FN];
+    if constexpr (FUSED) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) bias[j] = bias_at(ep, min(col0 + j * 32 + lr, N - 1));
+    }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -795,11 +815,16 @@ tile_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
             for (int e = 0; e < 16; ++e) {
                 const int r = 8 * (e / 4) + 4 * g + (e % 4);
                 otype v;
-                if constexpr (OUT == OF32) v = acc[i][j][e];
+                if constexpr (FUSED) v = acc[i][j][e] + bias[j];
+                else if constexpr (OUT == OF32) v = acc[i][j][e];
                 else v = f32_to_bf16(acc[i][j][e]);
                 *(otype *)(stage + r * PITCH + (j * 32 + lr) * OS) = v;
             }
         const int row0 = m0 + wm * WTM + i * 32;
+        if constexpr (FUSED) {
+            fused_band<OUT, WTN, PITCH>(ep, stage, C, row0, col0, M, N, lane);
+            continue;
+        }
         constexpr int NIT = (32 * CPR + 63) / 64;
 #pragma unroll
         for (int it = 0; it < NIT; ++it) {

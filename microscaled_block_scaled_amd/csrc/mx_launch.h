@@ -12,6 +12,8 @@
 #include "mx_kernels.h"
 #include "mx_host.h"
 
+namespace mx { struct Epilogue; }      // mx_epilogue.h
+
 namespace mxhost {
 
 // Split-K slices are whole 512-K scale periods.
@@ -104,6 +106,14 @@ inline bool decode_fits(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K)
 bool launch_decode(int fmt_a, int fmt_b, int out_dtype, const void *A, const void *As,
                    const void *B, const void *Bs, void *C, int64_t M, int64_t N, int64_t K,
                    hipStream_t s);
+
+// Whether the fused epilogue is compiled for a pair of formats (MX_FMT_* or
+// kFmtBF16), and the plan's kernel with it (both defined in mxfused.hip).
+// launch_fused returns false if the plan's tile is not compiled.
+bool fused_pair(int fmt_a, int fmt_b);
+bool launch_fused(int fmt_a, int fmt_b, const mx_plan_t &p, int out_dtype, const void *A,
+                  const void *As, const void *B, const void *Bs, void *C, int64_t M, int64_t N,
+                  int64_t K, float *W, const mx::Epilogue &ep, hipStream_t s);
 
 // Grouped launches: one tile shape (kTiles[t]) for every group, the group
 // table in the kernel arguments, no K split.

@@ -1,0 +1,287 @@
+// mx_moe.h -- gfx950 device code of expert routing around the grouped GEMM:
+// (token, choice) pairs sorted by expert, token rows gathered into expert
+// order, expert rows combined back with weights, and the gradient of the
+// combination.
+//
+// Pair i = token * top + choice.  The sort is stable: an expert's rows are in
+// the order of their pairs, so nothing depends on timing.  row_of[i] is pair
+// i's row in expert order; a pair whose id is no expert (a padding token, a
+// dropped choice) comes after all experts, at row r, and has row_of = -1 - r.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx_rowops.h"
+
+namespace mx {
+
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortBins = kMaxGroups + 1;       // the experts, and no expert
+
+struct SortArgs {
+    const void *ids;
+    int64_t *group_rows;
+    int32_t *row_of;
+    int32_t *counts;             // chunks x bins: pairs of each bin in each chunk
+    int64_t n, chunk;            // pairs, and pairs per workgroup (a multiple of kSortThreads)
+    int experts, id64;
+};
+
+// Bin of pair i (i < n): its expert, or `experts` for none.
+__device__ __forceinline__ int sort_bin(const SortArgs &a, int64_t i)
+{
+    const int64_t id = a.id64 ? ((const int64_t *)a.ids)[i] : (int64_t)((const int32_t *)a.ids)[i];
+    return id >= 0 && id < a.experts ? (int)id : a.experts;
+}
+
+// The lanes of the wave that hold the same bin as this lane (dead lanes
+// match nobody): one ballot per bit of the bin number.
+__device__ __forceinline__ uint64_t same_bin(int bin, bool live, int bits)
+{
+    uint64_t m = __ballot(live);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (bin >> b) & 1;
+        const uint64_t v = __ballot(one);
+        m &= one ? v : ~v;
+    }
+    return m;
+}
+
+// Adds this wave's share of the workgroup's chunk, a run of chunk / 16
+// consecutive pairs, to its row of per-wave bin counts in LDS.
+__device__ __forceinline__ void sort_count(const SortArgs &a, int (*cnt)[kSortBins + 1], int bits)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int i = threadIdx.x; i < kSortWaves * (kSortBins + 1); i += kSortThreads)
+        ((int *)cnt)[i] = 0;
+    __syncthreads();
+    const int64_t per = a.chunk / kSortWaves;
+    const int64_t lo = blockIdx.x * a.chunk + wave * per, hi = min(lo + per, a.n);
+    for (int64_t i = lo + lane; i - lane < hi; i += 64) {
+        const bool live = i < hi;
+        const int bin = live ? sort_bin(a, i) : 0;
+        const uint64_t m = same_bin(bin, live, bits);
+        if (live && (m & ((1ull << lane) - 1)) == 0) cnt[wave][bin] += __popcll(m);
+    }
+    __syncthreads();
+}
+
+// First of two launches for many pairs: the bin counts of each chunk.
+__global__ void __launch_bounds__(kSortThreads)
+moe_count(SortArgs a)
+{
+    __shared__ int cnt[kSortWaves][kSortBins + 1];
+    sort_count(a, cnt, 32 - __clz(a.experts));
+    const int bins = a.experts + 1;
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+        int t = 0;
+        for (int w = 0; w < kSortWaves; ++w) t += cnt[w][b];
+        a.counts[(int64_t)blockIdx.x * bins + b] = t;
+    }
+}
+
+// A counting sort: the first row of every (bin, chunk, wave) is the number
+// of pairs before it in that order; each wave then walks its run of pairs,
+// 64 at a time, and a pair's row is its wave's next row of the bin plus the
+// earlier lanes of the same bin.  MANY: one workgroup per chunk, the other
+// chunks' counts from moe_count; otherwise the one workgroup has them all.
+template <bool MANY>
+__global__ void __launch_bounds__(kSortThreads)
+moe_sort(SortArgs a)
+{
+    __shared__ int cnt[kSortWaves][kSortBins + 1];
+    __shared__ int scan[kSortBins];
+    const int bits = 32 - __clz(a.experts), bins = a.experts + 1;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    sort_count(a, cnt, bits);
+    int before = 0, total = 0;                   // this bin's pairs in earlier chunks, in all
+    if (tid < bins) {
+        if constexpr (MANY) {
+            for (int c = 0; c < (int)gridDim.x; ++c) {
+                const int v = a.counts[(int64_t)c * bins + tid];
+                total += v;
+                before += c < (int)blockIdx.x ? v : 0;
+            }
+        } else {
+            for (int w = 0; w < kSortWaves; ++w) total += cnt[w][tid];
+        }
+        scan[tid] = total;
+        if (blockIdx.x == 0 && tid < a.experts) a.group_rows[tid] = total;
+    }
+    __syncthreads();
+    for (int d = 1; d < bins; d <<= 1) {         // inclusive sums over the bins
+        const int v = tid >= d && tid < bins ? scan[tid - d] : 0;
+        __syncthreads();
+        if (tid < bins) scan[tid] += v;
+        __syncthreads();
+    }
+    if (tid < bins) {
+        int at = scan[tid] - total + before;
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int v = cnt[w][tid];
+            cnt[w][tid] = at;
+            at += v;
+        }
+    }
+    __syncthreads();
+    const int64_t per = a.chunk / kSortWaves;
+    const int64_t lo = blockIdx.x * a.chunk + wave * per, hi = min(lo + per, a.n);
+    for (int64_t i = lo + lane; i - lane < hi; i += 64) {
+        const bool live = i < hi;
+        const int bin = live ? sort_bin(a, i) : 0;
+        const uint64_t m = same_bin(bin, live, bits);
+        const int ahead = __popcll(m & ((1ull << lane) - 1));
+        const int row = live ? cnt[wave][bin] + ahead : 0;
+        // every lane has read its bin's next row before its first lane moves it
+        __builtin_amdgcn_wave_barrier();
+        if (live && ahead == 0) cnt[wave][bin] += __popcll(m);
+        __builtin_amdgcn_wave_barrier();
+        if (live) a.row_of[i] = bin == a.experts ? -1 - row : row;
+    }
+}
+
+// Rows of x (row_bytes each, and scale_bytes of scales) copied to the rows of
+// their pairs; rows of pairs without an expert are filled with zeros.  Each
+// token row is read once and written `top` times.  A wave takes 64 units of
+// U bytes of one token's row.
+struct GatherArgs {
+    const uint8_t *x, *s;
+    uint8_t *xs, *ss;
+    const int32_t *row_of;
+    int64_t items, n, ldx, lds;                  // n: pairs; pitches in bytes
+    int top, row_bytes, scale_bytes;
+    int row_segs, segs;                          // waves per token: rows, and rows + scales
+};
+
+template <int U> struct unit;
+template <> struct unit<16> { typedef v4i t; };
+template <> struct unit<4> { typedef int t; };
+template <> struct unit<1> { typedef uint8_t t; };
+
+template <int U>
+__device__ __forceinline__ void gather_seg(const uint8_t *src, uint8_t *dst, int bytes, int at,
+                                           const int32_t *row_of, int top, int64_t n)
+{
+    typedef typename unit<U>::t T;
+    if (at >= bytes) return;
+    const T v = *(const T *)(src + at);
+    for (int j = 0; j < top; ++j) {
+        const int r = row_of[j];
+        const int64_t to = r < 0 ? -1 - (int64_t)r : r;
+        if (to >= n) continue;
+        *(T *)(dst + to * bytes + at) = r < 0 ? T{} : v;
+    }
+}
+
+template <int U, int US>
+__global__ void __launch_bounds__(256)
+moe_gather(GatherArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t waves = (int64_t)gridDim.x * 4;
+    for (int64_t it = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+         it < a.items; it += waves) {
+        const int64_t t = it / a.segs;
+        const int seg = (int)(it - t * a.segs);
+        const int32_t *row_of = a.row_of + t * a.top;
+        if (seg < a.row_segs)
+            gather_seg<U>(a.x + t * a.ldx, a.xs, a.row_bytes, (seg * 64 + lane) * U, row_of,
+                          a.top, a.n);
+        else
+            gather_seg<US>(a.s + t * a.lds, a.ss, a.scale_bytes,
+                           ((seg - a.row_segs) * 64 + lane) * US, row_of, a.top, a.n);
+    }
+}
+
+// out[t] = r[t] + sum over choices j, in order, of w[t][j] * y[row_of[t][j]];
+// pairs without an expert add nothing and nothing of theirs is read.  Without
+// weights each counts 1, which is the gradient of the gather.
+struct CombineArgs {
+    const void *y, *r;
+    const float *w;
+    const int32_t *row_of;
+    void *out;
+    int64_t items, rows, ldy, ldr;               // rows of y; pitches in elements
+    int top, width, segs;
+};
+
+template <int IN>
+__global__ void __launch_bounds__(256)
+moe_combine(CombineArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t waves = (int64_t)gridDim.x * 4;
+    for (int64_t it = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+         it < a.items; it += waves) {
+        const int64_t t = it / a.segs;
+        const int col = ((int)(it - t * a.segs) * 64 + lane) * 8;
+        if (col >= a.width) continue;
+        float acc[8] = {};
+        for (int j = 0; j < a.top; ++j) {
+            const int r = a.row_of[t * a.top + j];
+            if (r < 0 || r >= a.rows) continue;
+            const float w = a.w ? a.w[t * a.top + j] : 1.f;
+            float v[8];
+            unpack8<IN>(load8<IN>(a.y, r * a.ldy + col), v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(v[i], w, acc[i]);
+        }
+        if (a.r) {
+            float v[8];
+            unpack8<IN>(load8<IN>(a.r, t * a.ldr + col), v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] += v[i];
+        }
+        store8<IN>(a.out, t * a.width + col, pack8<IN>(acc));
+    }
+}
+
+// Gradient of the combination: dy[row_of[t][j]] = w[t][j] * dout[t] (zeros in
+// the rows of pairs without an expert) and dw[t][j] = <dout[t], y[row]> (0
+// without an expert).  A wave takes one pair at a time; the waves of a
+// workgroup share a token's dout row through the L1.
+struct CombineGradArgs {
+    const void *dout, *y;
+    const float *w;
+    const int32_t *row_of;
+    void *dy;
+    float *dw;
+    int64_t n, rows, lddo, ldy;
+    int top, width;
+};
+
+template <int IN>
+__global__ void __launch_bounds__(256)
+moe_combine_grad(CombineGradArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t waves = (int64_t)gridDim.x * 4;
+    for (int64_t i = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+         i < a.n; i += waves) {
+        const int64_t t = i / a.top;
+        const int r = a.row_of[i];
+        const int64_t to = r < 0 ? -1 - (int64_t)r : r;
+        const bool live = r >= 0 && to < a.rows;
+        const float w = live && a.w ? a.w[i] : 1.f;
+        float dot = 0.f;
+        if (to < a.rows)
+            for (int col = lane * 8; col < a.width; col += 512) {
+                float d[8] = {}, v[8];
+                if (live) {
+                    unpack8<IN>(load8<IN>(a.dout, t * a.lddo + col), d);
+                    unpack8<IN>(load8<IN>(a.y, to * a.ldy + col), v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        dot = fmaf(d[e], v[e], dot);
+                        d[e] *= w;
+                    }
+                }
+                store8<IN>(a.dy, to * a.width + col, pack8<IN>(d));
+            }
+        dot = block_sum<64>(dot, nullptr);
+        if (lane == 0) a.dw[i] = dot;
+    }
+}
+
+}  // namespace mx

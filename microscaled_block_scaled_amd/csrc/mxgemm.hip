@@ -14,6 +14,7 @@
 #include "mxgemm.h"
 #include "mx_kernels.h"
 #include "mx_decode.h"
+#include "mx_epilogue.h"
 #include "mx_quant.h"
 #include "mx_quant6.h"
 #include "mx_ceiling.h"
@@ -255,10 +256,11 @@ int device_scratch(int dev, void **ptr)
 
 // Checks that need no device, then the device check, then the launch.  With
 // noalloc the split-K workspace is the device's fixed scratch instead of a
-// stream-ordered allocation.
+// stream-ordered allocation; ep, if given, is the fused epilogue.
 int run_plan(const mx_plan_t &plan, int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K,
              const void *A, const void *A_scale, const void *B, const void *B_scale,
-             void *C, int out_dtype, void *stream, bool noalloc = false)
+             void *C, int out_dtype, void *stream, bool noalloc = false,
+             const mx::Epilogue *ep = nullptr)
 {
     const bool scaled = fmt_a != kFmtBF16;
     if (!A || !B || !C || (scaled && (!A_scale || !B_scale))) return MX_ERR_NULL;
@@ -288,7 +290,10 @@ int run_plan(const mx_plan_t &plan, int fmt_a, int fmt_b, int64_t M, int64_t N, 
     }
     bool launched;
     const int o = out_dtype;
-    if (plan.variant == MX_VARIANT_DECODE)
+    if (ep)
+        launched = launch_fused(fmt_a, fmt_b, plan, o, A, A_scale, B, B_scale, C, M, N, K, W,
+                                *ep, s);
+    else if (plan.variant == MX_VARIANT_DECODE)
         launched = launch_decode(fmt_a, fmt_b, o, A, A_scale, B, B_scale, C, M, N, K, s);
     else if (!scaled)
         launched = launch<mx::B16, mx::B16>(plan, o, A, nullptr, B, nullptr, C, M, N, K, W, s);
@@ -340,6 +345,10 @@ extern "C" const char *mx_strerror(int code)
     case MX_ERR_IN_DTYPE: return "unsupported input type (expected MX_IN_FP32 or MX_IN_BF16)";
     case MX_ERR_SCRATCH: return "split-K workspace larger than the fixed scratch of the "
                                 "no-allocation entry point (MX_NOALLOC_SCRATCH_BYTES)";
+    case MX_ERR_ROW_SHAPE: return "bad shape of a row, routing or epilogue operator (sizes and pitches "
+                                  "as mxgemm.h says)";
+    case MX_ERR_WORKSPACE: return "workspace smaller than the operator needs";
+    case MX_ERR_ACT: return "unknown activation";
     default: return "unknown error code";
     }
 }
@@ -450,6 +459,60 @@ extern "C" int mx_gemm_bf16(int64_t M, int64_t N, int64_t K, const void *A, cons
     }
     return run_plan(plan, kFmtBF16, kFmtBF16, M, N, K, A, nullptr, B, nullptr, C, out_dtype,
                     stream);
+}
+
+namespace {
+
+// Checks of a fused epilogue; fills ep.
+int check_epilogue(int64_t N, int out_dtype, const void *bias, int bias_dtype, int act,
+                   const void *residual, int64_t ldr, mx::Epilogue *ep)
+{
+    if (act < MX_ACT_NONE || act > MX_ACT_GELU_TANH) return MX_ERR_ACT;
+    if (bias && bias_dtype != MX_IN_FP32 && bias_dtype != MX_IN_BF16) return MX_ERR_IN_DTYPE;
+    if (residual && (ldr < N || ldr > MX_MAX_DIM)) return MX_ERR_ROW_SHAPE;
+    const uintptr_t bias_align = bias_dtype == MX_IN_BF16 ? 2 : 4;
+    if ((bias && !aligned(bias, bias_align)) || !aligned(residual, 16)) return MX_ERR_ALIGN;
+    *ep = mx::Epilogue{bias, residual, ldr, bias_dtype == MX_IN_BF16, act};
+    return MX_OK;
+}
+
+}  // namespace
+
+extern "C" int mx_gemm_fused(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K,
+                             const void *A, const void *A_scale, const void *B,
+                             const void *B_scale, const void *bias, int bias_dtype, int act,
+                             const void *residual, int64_t ldr, void *C, int out_dtype,
+                             void *stream)
+{
+    int rc = check_args(fmt_a, M, N, K, out_dtype);
+    if (rc != MX_OK) return rc;
+    if (fmt_b < MX_FMT_E2M1 || fmt_b > MX_FMT_E3M2 || !fused_pair(fmt_a, fmt_b))
+        return MX_ERR_FORMAT;
+    mx::Epilogue ep;
+    rc = check_epilogue(N, out_dtype, bias, bias_dtype, act, residual, ldr, &ep);
+    if (rc != MX_OK) return rc;
+    mx_plan_t plan;
+    plan_for(fmt_a, fmt_b, M, N, K, &plan);
+    if (plan.workgroups > kMaxGrid) return MX_ERR_SHAPE;
+    return run_plan(plan, fmt_a, fmt_b, M, N, K, A, A_scale, B, B_scale, C, out_dtype, stream,
+                    false, &ep);
+}
+
+extern "C" int mx_gemm_bf16_fused(int64_t M, int64_t N, int64_t K, const void *A, const void *B,
+                                  const void *bias, int bias_dtype, int act,
+                                  const void *residual, int64_t ldr, void *C, int out_dtype,
+                                  void *stream)
+{
+    int rc = check_args_bf16(M, N, K, out_dtype);
+    if (rc != MX_OK) return rc;
+    mx::Epilogue ep;
+    rc = check_epilogue(N, out_dtype, bias, bias_dtype, act, residual, ldr, &ep);
+    if (rc != MX_OK) return rc;
+    mx_plan_t plan;
+    fill_plan(choose_tile(M, N, K), M, N, K, &plan);
+    if (plan.workgroups > kMaxGrid) return MX_ERR_SHAPE;
+    return run_plan(plan, kFmtBF16, kFmtBF16, M, N, K, A, nullptr, B, nullptr, C, out_dtype,
+                    stream, false, &ep);
 }
 
 extern "C" int mx_quantize(int fmt, int in_dtype, int64_t rows, int64_t K,

@@ -64,36 +64,33 @@ def declare(L):
         f.restype, f.argtypes = res, args
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
-class _Call(contextlib.AbstractContextManager):
-    """The device and stream of one call: inside it the device is current,
-    and allocations belong to ``stream`` when that is not the current one."""
+_HERE = contextlib.nullcontext()
 
-    __slots__ = ("stream", "_stack")
 
-    def __init__(self, device, stream):
-        torch = _torch()
-        current = torch.cuda.current_stream(device)
-        self.stream = current.cuda_stream if stream is None else int(stream)
-        self._stack = None
-        if self.stream != current.cuda_stream:
-            self._stack = [torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device))]
-        elif torch.cuda.current_device() != device.index:
-            self._stack = [torch.cuda.device(device)]
-
-    def __enter__(self):
-        if self._stack is not None:
-            self._stack[0].__enter__()
-        return self.stream or None
-
-    def __exit__(self, *exc):
-        if self._stack is not None:
-            self._stack[0].__exit__(*exc)
-        return False
+def _enter(device, stream):
+    """(context, stream handle) of one call: inside the context the device is
+    current, and allocations belong to ``stream`` when that is not the current
+    one."""
+    torch = _torch()
+    index = device.index
+    current = torch._C._cuda_getCurrentRawStream(index)
+    if stream is not None and int(stream) != current:
+        ext = torch.cuda.ExternalStream(int(stream), device)
+        return torch.cuda.stream(ext), int(stream) or None
+    if torch._C._cuda_getDevice() != index:
+        return torch.cuda.device(device), current or None
+    return _HERE, current or None
 
 
 def _check(rc):
@@ -124,27 +121,29 @@ def _rows(t, name, width=None, rows=None, dtype=None, device=None):
     """A 2-D tensor of rows with contiguous elements (any row pitch): its
     pitch."""
     _tensor(t, name, device)
-    if t.dim() != 2:
-        raise ValueError("%s must be 2-D" % name)
     shape = t.shape
-    if (width is not None and shape[1] != width) or (rows is not None and shape[0] != rows):
+    if len(shape) != 2:
+        raise ValueError("%s must be 2-D" % name)
+    n, w = shape
+    if (width is not None and w != width) or (rows is not None and n != rows):
         raise ValueError("%s has shape %s, expected (%s, %s)"
                          % (name, tuple(shape), rows if rows is not None else "rows",
                             width if width is not None else "width"))
     if dtype is not None and t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if shape[1] > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and w > 1:
         raise ValueError("%s must have contiguous rows" % name)
-    if shape[0] <= 1:
-        return shape[1]                      # the pitch of one row means nothing
-    if t.stride(0) < shape[1]:
+    if n <= 1:
+        return w                             # the pitch of one row means nothing
+    if ld < w:
         raise ValueError("%s must have rows that do not overlap" % name)
-    return t.stride(0)
+    return ld
 
 
 def _vector(t, name, n, device, dtypes):
     _tensor(t, name, device)
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s must be a contiguous vector of %d values" % (name, n))
     if t.dtype not in dtypes:
         raise ValueError("%s must be one of %s, got %s" % (name, dtypes, t.dtype))
@@ -179,14 +178,15 @@ def mx_rmsnorm_quantize(x, weight, fmt, residual=None, eps=1e-6, need_y=False, n
     ldr = 0
     if residual is not None:
         ldr = _rows(residual, "residual", width, rows, x.dtype, dev)
-    with _Call(dev, stream) as s:
-        h = x if residual is None else torch.empty((rows, width), dtype=x.dtype, device=dev)
+    ctx, s = _enter(dev, stream)
+    with ctx:
+        h = x if residual is None else x.new_empty((rows, width))
         q = qs = y = rstd = None
         if fmt is not None:
             q = torch.empty((rows, _m._row_bytes(_fmt(fmt), width)), dtype=torch.uint8, device=dev)
             qs = torch.empty((rows, width // 32), dtype=torch.uint8, device=dev)
         if need_y:
-            y = torch.empty((rows, width), dtype=x.dtype, device=dev)
+            y = x.new_empty((rows, width))
         if need_rstd:
             rstd = torch.empty(rows, dtype=torch.float32, device=dev)
         _check(_m.lib().mx_rmsnorm_quantize(
@@ -211,8 +211,9 @@ def mx_rmsnorm_backward(dy, h, rstd, weight, dh=None, need_dw=True, stream=None)
     _vector(weight, "weight", width, dev, (torch.float32, torch.bfloat16))
     _vector(rstd, "rstd", rows, dev, (torch.float32,))
     L = _m.lib()
-    with _Call(dev, stream) as s:
-        dx = torch.empty((rows, width), dtype=h.dtype, device=dev)
+    ctx, s = _enter(dev, stream)
+    with ctx:
+        dx = h.new_empty((rows, width))
         dw = ws = None
         nbytes = 0
         if need_dw:
@@ -239,7 +240,8 @@ def mx_swiglu_quantize(gate_up, fmt, stream=None):
     width = two // 2
     dev = gate_up.device
     code = _dtype_code(gate_up, "gate_up")
-    with _Call(dev, stream) as s:
+    ctx, s = _enter(dev, stream)
+    with ctx:
         q = torch.empty((rows, _m._row_bytes(_fmt(fmt), width)), dtype=torch.uint8, device=dev)
         qs = torch.empty((rows, width // 32), dtype=torch.uint8, device=dev)
         _check(_m.lib().mx_swiglu_quantize(fmt, code, rows, width, gate_up.data_ptr(), ld,
@@ -258,8 +260,9 @@ def mx_swiglu_backward(dy, gate_up, stream=None):
     dev = gate_up.device
     code = _dtype_code(gate_up, "gate_up")
     lddy = _rows(dy, "dy", two // 2, rows, gate_up.dtype, dev)
-    with _Call(dev, stream) as s:
-        dgu = torch.empty((rows, two), dtype=gate_up.dtype, device=dev)
+    ctx, s = _enter(dev, stream)
+    with ctx:
+        dgu = gate_up.new_empty((rows, two))
         _check(_m.lib().mx_swiglu_backward(code, rows, two // 2, dy.data_ptr(), lddy,
                                            gate_up.data_ptr(), ld, dgu.data_ptr(), s))
     return dgu
@@ -283,7 +286,8 @@ def mx_moe_sort(ids, experts, stream=None):
     nbytes = L.mx_moe_sort_workspace(tokens, top, experts)
     if nbytes < 0:
         _m._raise(nbytes)
-    with _Call(dev, stream) as s:
+    ctx, s = _enter(dev, stream)
+    with ctx:
         group_rows = torch.empty(experts, dtype=torch.int64, device=dev)
         row_of = torch.empty((tokens, top), dtype=torch.int32, device=dev)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
@@ -316,11 +320,12 @@ def mx_moe_gather(plan, x, x_scale=None, stream=None):
         ssize = x_scale.element_size()
         lds = _rows(x_scale, "x_scale", rows=tokens, device=dev) * ssize
         sbytes = x_scale.shape[1] * ssize
-    with _Call(dev, stream) as s:
-        xs = torch.empty((tokens * top, x.shape[1]), dtype=x.dtype, device=dev)
+    ctx, s = _enter(dev, stream)
+    with ctx:
+        xs = x.new_empty((tokens * top, x.shape[1]))
         ss = None
         if x_scale is not None:
-            ss = torch.empty((tokens * top, x_scale.shape[1]), dtype=x_scale.dtype, device=dev)
+            ss = x_scale.new_empty((tokens * top, x_scale.shape[1]))
         _check(_m.lib().mx_moe_gather(tokens, top, row_of.data_ptr(), x.data_ptr(),
                                       x.shape[1] * size, ld * size, _ptr(x_scale), sbytes, lds,
                                       xs.data_ptr(), _ptr(ss), s))
@@ -351,8 +356,9 @@ def mx_moe_combine(plan, y, weights=None, residual=None, stream=None):
     if weights is not None:
         _weights(weights, row_of, dev)
     ldr = 0 if residual is None else _rows(residual, "residual", width, tokens, y.dtype, dev)
-    with _Call(dev, stream) as s:
-        out = torch.empty((tokens, width), dtype=y.dtype, device=dev)
+    ctx, s = _enter(dev, stream)
+    with ctx:
+        out = y.new_empty((tokens, width))
         _check(_m.lib().mx_moe_combine(code, tokens, top, width, row_of.data_ptr(), y.data_ptr(),
                                        y.shape[0], ldy, _ptr(weights), _ptr(residual), ldr,
                                        out.data_ptr(), s))
@@ -372,8 +378,9 @@ def mx_moe_combine_backward(plan, dout, y, weights, stream=None):
     width = y.shape[1]
     lddo = _rows(dout, "dout", width, tokens, y.dtype, dev)
     _weights(weights, row_of, dev)
-    with _Call(dev, stream) as s:
-        dy = torch.empty((y.shape[0], width), dtype=y.dtype, device=dev)
+    ctx, s = _enter(dev, stream)
+    with ctx:
+        dy = y.new_empty((y.shape[0], width))
         dw = torch.empty((tokens, top), dtype=torch.float32, device=dev)
         _check(_m.lib().mx_moe_combine_backward(
             code, tokens, top, width, row_of.data_ptr(), dout.data_ptr(), lddo, y.data_ptr(),
@@ -421,7 +428,8 @@ def mx_gemm_fused(a, a_scale, b, b_scale, fmt, bias=None, act=ACT_NONE, residual
         if t.device != dev:
             raise ValueError("all operands must be on the same device")
     bias_code, ldr = _epilogue(M, N, tdt, dev, bias, residual, out)
-    with _Call(dev, stream) as s:
+    ctx, s = _enter(dev, stream)
+    with ctx:
         if out is None:
             out = torch.empty((M, N), dtype=tdt, device=dev)
         _check(_m.lib().mx_gemm_fused(
@@ -445,7 +453,8 @@ def mx_gemm_bf16_fused(a, b, bias=None, act=ACT_NONE, residual=None, out_dtype=N
     if b.device != dev:
         raise ValueError("all operands must be on the same device")
     bias_code, ldr = _epilogue(M, N, tdt, dev, bias, residual, out)
-    with _Call(dev, stream) as s:
+    ctx, s = _enter(dev, stream)
+    with ctx:
         if out is None:
             out = torch.empty((M, N), dtype=tdt, device=dev)
         _check(_m.lib().mx_gemm_bf16_fused(M, N, K, a.data_ptr(), b.data_ptr(), _ptr(bias),

@@ -98,6 +98,7 @@ moe_sort(SortArgs a)
     int before = 0, total = 0;                   // this bin's pairs in earlier chunks, in all
     if (tid < bins) {
         if constexpr (MANY) {
+#pragma unroll 16
             for (int c = 0; c < (int)gridDim.x; ++c) {
                 const int v = a.counts[(int64_t)c * bins + tid];
                 total += v;
@@ -279,7 +280,7 @@ moe_combine_grad(CombineGradArgs a)
                 }
                 store8<IN>(a.dy, to * a.width + col, pack8<IN>(d));
             }
-        dot = block_sum<64>(dot, nullptr);
+        dot = wave_sum(dot);
         if (lane == 0) a.dw[i] = dot;
     }
 }

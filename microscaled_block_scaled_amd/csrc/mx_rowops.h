@@ -133,21 +133,41 @@ __device__ __forceinline__ void quantize8(const float (&v)[8], uint8_t *q, uint8
     }
 }
 
-// Sum over the workgroup of T threads, in a fixed order (lanes by halving
-// distance, then the waves in order); every thread gets it.  `part` is T / 64
-// floats of LDS that no thread is still reading.
-template <int T>
-__device__ __forceinline__ float block_sum(float v, float *part)
+// Sum over the wave, by halving distance; every lane gets it.
+__device__ __forceinline__ float wave_sum(float v)
 {
 #pragma unroll
     for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    if constexpr (T == 64) return v;
+    return v;
+}
+
+// Sum over the workgroup in a fixed order (each wave's, then the waves in
+// order); every thread gets it.  `part` is a float of LDS per wave that no
+// thread is still reading: two of them in turn need no other barrier.
+__device__ __forceinline__ float block_sum(float v, float *part)
+{
+    v = wave_sum(v);
+    const int waves = blockDim.x >> 6;
+    if (waves == 1) return v;
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
     float t = part[0];
-#pragma unroll
-    for (int w = 1; w < T / 64; ++w) t += part[w];
+    for (int w = 1; w < waves; ++w) t += part[w];
     return t;
+}
+
+// 8 weights as loaded, FP32 or BF16 by a uniform flag.
+__device__ __forceinline__ raw8<IN_F32> load_weight(const void *w, int col, int bf16)
+{
+    raw8<IN_F32> r;
+    if (bf16) r.q[0] = load8<IN_BF16>(w, col).q[0];
+    else r = load8<IN_F32>(w, col);
+    return r;
+}
+__device__ __forceinline__ void unpack_weight(const raw8<IN_F32> &r, int bf16, float (&v)[8])
+{
+    if (bf16) unpack8<IN_BF16>(raw8<IN_BF16>{{r.q[0]}}, v);
+    else unpack8<IN_F32>(r, v);
 }
 
 // What the norm reads and writes (pitches in elements of the rows' type; y,
@@ -166,57 +186,63 @@ struct NormArgs {
 // y = h * rstd * w; (q, s) = MX(y) from the unrounded y.  The statistic is of
 // the rounded h, which is what the next layer and the gradient read.
 //
-// One workgroup of T threads per row, the row in registers (C chunks of 8 per
-// thread, chunk c of thread t holding values 8 (c T + t) ..), so the row is
-// read once for both the sum and the norm.
-template <int IN, int F, int T, int C>
-__global__ void __launch_bounds__(T)
+// One workgroup per row, the row in registers (C chunks of 8 per thread,
+// chunk c of thread t holding values 8 (c T + t) .., T threads), so the row is
+// read once for both the sum and the norm.  The weights are loaded before the
+// sum is known, beside the row itself.
+template <int IN, int F, int MAXT, int C>
+__global__ void __launch_bounds__(MAXT)
 norm_quantize(NormArgs a)
 {
-    __shared__ float part[2][T / 64];
-    const int tid = threadIdx.x;
+    __shared__ float part[2][MAXT / 64];
+    const int tid = threadIdx.x, T = blockDim.x;
     int flip = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-    raw8<IN> hv[C];
-    float sum = 0.f;
+        raw8<IN> hv[C], rv[C];
+        raw8<IN_F32> wv[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int col = (c * T + tid) * 8;
-        if (col >= a.width) continue;
-        hv[c] = load8<IN>(a.x, row * a.ldx + col);
-        if (a.r) {
-            float x[8], r[8];
-            unpack8<IN>(hv[c], x);
-            unpack8<IN>(load8<IN>(a.r, row * a.ldr + col), r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] += r[i];
-            hv[c] = pack8<IN>(x);
-            store8<IN>(a.h, row * a.width + col, hv[c]);
+        for (int c = 0; c < C; ++c) {
+            const int col = (c * T + tid) * 8;
+            if (col >= a.width) continue;
+            hv[c] = load8<IN>(a.x, row * a.ldx + col);
+            if (a.r) rv[c] = load8<IN>(a.r, row * a.ldr + col);
+            wv[c] = load_weight(a.w, col, a.w_bf16);
         }
-        float h[8];
-        unpack8<IN>(hv[c], h);
+        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(h[i], h[i], sum);
-    }
-    sum = block_sum<T>(sum, part[flip]);
-    const float rstd = 1.f / sqrtf(sum / (float)a.width + a.eps);
-    if (a.rstd && tid == 0) a.rstd[row] = rstd;
+        for (int c = 0; c < C; ++c) {
+            const int col = (c * T + tid) * 8;
+            if (col >= a.width) continue;
+            float h[8];
+            if (a.r) {
+                float r[8];
+                unpack8<IN>(hv[c], h);
+                unpack8<IN>(rv[c], r);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int col = (c * T + tid) * 8;
-        if (col >= a.width) continue;
-        float h[8], w[8], y[8];
-        unpack8<IN>(hv[c], h);
-        if (a.w_bf16) unpack8<IN_BF16>(load8<IN_BF16>(a.w, col), w);
-        else unpack8<IN_F32>(load8<IN_F32>(a.w, col), w);
+                for (int i = 0; i < 8; ++i) h[i] += r[i];
+                hv[c] = pack8<IN>(h);
+                store8<IN>(a.h, row * a.width + col, hv[c]);
+            }
+            unpack8<IN>(hv[c], h);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = h[i] * rstd * w[i];
-        if (a.y) store8<IN>(a.y, row * a.width + col, pack8<IN>(y));
-        if (a.q) {
+            for (int i = 0; i < 8; ++i) sum = fmaf(h[i], h[i], sum);
+        }
+        sum = block_sum(sum, part[flip]);
+        const float rstd = 1.f / sqrtf(sum / (float)a.width + a.eps);
+        if (a.rstd && tid == 0) a.rstd[row] = rstd;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = (c * T + tid) * 8;
+            if (col >= a.width) continue;
+            float h[8], w[8], y[8];
+            unpack8<IN>(hv[c], h);
+            unpack_weight(wv[c], a.w_bf16, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = h[i] * rstd * w[i];
             const int64_t at = row * a.width + col;
-            quantize8<F>(y, a.q + at / 8 * mx8<F>::bytes, a.s + at / 32, (tid & 3) == 0);
+            if (a.y) store8<IN>(a.y, at, pack8<IN>(y));
+            if (a.q) quantize8<F>(y, a.q + at / 8 * mx8<F>::bytes, a.s + at / 32, (tid & 3) == 0);
         }
-    }
     }
 }
 
@@ -236,30 +262,49 @@ struct NormGradArgs {
 };
 
 // Workgroup b takes rows b, b + gridDim.x, ...; a thread keeps its columns'
-// dw sums in registers over all of them and writes them once.
-template <int IN, int T, int C>
-__global__ void __launch_bounds__(T)
+// weights and dw sums in registers over all of them.  The next row's loads
+// are issued before the current row's sum is joined over the workgroup, so
+// memory stays busy across the barrier.
+template <int IN, int MAXT, int C>
+__global__ void __launch_bounds__(MAXT)
 norm_grad(NormGradArgs a)
 {
-    __shared__ float part[2][T / 64];
-    const int tid = threadIdx.x;
+    __shared__ float part[2][MAXT / 64];
+    const int tid = threadIdx.x, T = blockDim.x;
     float dw[C][8] = {};
-    int flip = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-        const float rstd = a.rstd[row];
-        raw8<IN> hv[C], gv[C];
-        float dot = 0.f;
+    raw8<IN_F32> wv[C];
+    raw8<IN> gv[C], hv[C], dv[C];
+    float rs = 0.f;
+    auto load_row = [&](int64_t row) {
+        rs = a.rstd[row];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = (c * T + tid) * 8;
             if (col >= a.width) continue;
             gv[c] = load8<IN>(a.dy, row * a.lddy + col);
             hv[c] = load8<IN>(a.h, row * a.ldh + col);
+            if (a.dh) dv[c] = load8<IN>(a.dh, row * a.lddh + col);
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = (c * T + tid) * 8;
+        if (col < a.width) wv[c] = load_weight(a.w, col, a.w_bf16);
+    }
+    if (blockIdx.x < a.rows) load_row(blockIdx.x);
+    int flip = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
+        const float rstd = rs;
+        float dot = 0.f;
+        raw8<IN> g0[C], h0[C], d0[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            g0[c] = gv[c], h0[c] = hv[c], d0[c] = dv[c];
+            if ((c * T + tid) * 8 >= a.width) continue;
             float g[8], h[8], w[8];
             unpack8<IN>(gv[c], g);
             unpack8<IN>(hv[c], h);
-            if (a.w_bf16) unpack8<IN_BF16>(load8<IN_BF16>(a.w, col), w);
-            else unpack8<IN_F32>(load8<IN_F32>(a.w, col), w);
+            unpack_weight(wv[c], a.w_bf16, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float xhat = h[i] * rstd;
@@ -267,17 +312,17 @@ norm_grad(NormGradArgs a)
                 dw[c][i] = fmaf(g[i], xhat, dw[c][i]);
             }
         }
-        const float mean = block_sum<T>(dot, part[flip]) / (float)a.width;
+        if (row + gridDim.x < a.rows) load_row(row + gridDim.x);
+        const float mean = block_sum(dot, part[flip]) / (float)a.width;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = (c * T + tid) * 8;
             if (col >= a.width) continue;
             float g[8], h[8], w[8], d[8] = {};
-            unpack8<IN>(gv[c], g);
-            unpack8<IN>(hv[c], h);
-            if (a.w_bf16) unpack8<IN_BF16>(load8<IN_BF16>(a.w, col), w);
-            else unpack8<IN_F32>(load8<IN_F32>(a.w, col), w);
-            if (a.dh) unpack8<IN>(load8<IN>(a.dh, row * a.lddh + col), d);
+            unpack8<IN>(g0[c], g);
+            unpack8<IN>(h0[c], h);
+            unpack_weight(wv[c], a.w_bf16, w);
+            if (a.dh) unpack8<IN>(d0[c], d);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 d[i] = fmaf(fmaf(-(h[i] * rstd), mean, g[i] * w[i]), rstd, d[i]);
@@ -302,6 +347,7 @@ column_sum(const float *__restrict__ part, float *__restrict__ dw, int n, int wi
     const int cx = threadIdx.x & 7, ry = threadIdx.x >> 3;
     const int col = blockIdx.x * 32 + cx * 4;
     v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int r = ry; r < n; r += 32) acc += *(const v4f *)(part + (int64_t)r * width + col);
     sums[ry][cx] = acc;
     __syncthreads();

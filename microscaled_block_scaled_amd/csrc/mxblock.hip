@@ -53,23 +53,21 @@ void with_fmt(int dtype, int fmt, Fn f)
     }
 }
 
-// Calls f(T, C): threads of a row's workgroup and 8-value chunks per thread,
-// the fewest that hold a row of `width`.
+// Calls f(MAXT, C, threads): chunks of 8 values per thread, the threads of a
+// row's workgroup, and the most threads of that kernel.  Few rows take one
+// chunk per thread (the most loads in flight per row), many rows two, longer
+// rows what 512 or 1024 threads need.
 template <typename Fn>
-void with_row(int64_t width, Fn f)
+void with_row(int64_t rows, int64_t width, Fn f)
 {
-#define MX_ROW(T_, C_)                                                                     \
-    if (width <= T_ * C_ * 8) {                                                            \
-        f(std::integral_constant<int, T_>{}, std::integral_constant<int, C_>{});           \
-        return;                                                                            \
-    }
-    MX_ROW(64, 1)
-    MX_ROW(256, 1)
-    MX_ROW(256, 2)
-    MX_ROW(256, 4)
-    MX_ROW(512, 4)
-    MX_ROW(1024, 4)
-    MX_ROW(1024, 8)
+    const int64_t chunks = width / 8;
+    auto go = [&](auto t, auto c) { f(t, c, (int)(cdiv(chunks, 64 * c()) * 64)); };
+#define MX_ROW(T_, C_) go(std::integral_constant<int, T_>{}, std::integral_constant<int, C_>{})
+    if (chunks <= 1024 && rows <= 2 * kCUs) MX_ROW(1024, 1);
+    else if (chunks <= 1024) MX_ROW(512, 2);
+    else if (chunks <= 2048) MX_ROW(512, 4);
+    else if (chunks <= 4096) MX_ROW(1024, 4);
+    else MX_ROW(1024, 8);
 #undef MX_ROW
 }
 
@@ -118,9 +116,9 @@ extern "C" int mx_rmsnorm_quantize(int fmt, int dtype, int w_dtype, int64_t rows
     const mx::NormArgs a{X, R, W, H, Y, (uint8_t *)Q, (uint8_t *)Q_scale, rstd, rows, ldx, ldr,
                          (int)width, w_dtype == MX_IN_BF16, eps};
     with_fmt(dtype, Q ? fmt : MX_FMT_E4M3, [&](auto in, auto f) {
-        with_row(width, [&](auto t, auto c) {
+        with_row(rows, width, [&](auto t, auto c, int threads) {
             hipLaunchKernelGGL((mx::norm_quantize<in(), f(), t(), c()>), dim3(stride_grid(rows)),
-                               dim3(t()), 0, (hipStream_t)stream, a);
+                               dim3(threads), 0, (hipStream_t)stream, a);
         });
     });
     return launched();
@@ -160,13 +158,13 @@ extern "C" int mx_rmsnorm_backward(int dtype, int w_dtype, int64_t rows, int64_t
     const mx::NormGradArgs a{dY, H, W, dH, rstd, dX, dW ? (float *)workspace : nullptr, rows,
                              lddy, ldh, lddh, (int)width, w_dtype == MX_IN_BF16};
     if (groups)
-        with_row(width, [&](auto t, auto c) {
+        with_row(rows, width, [&](auto t, auto c, int threads) {
             if (dtype == MX_IN_FP32)
                 hipLaunchKernelGGL((mx::norm_grad<mx::IN_F32, t(), c()>), dim3((unsigned)groups),
-                                   dim3(t()), 0, s, a);
+                                   dim3(threads), 0, s, a);
             else
                 hipLaunchKernelGGL((mx::norm_grad<mx::IN_BF16, t(), c()>), dim3((unsigned)groups),
-                                   dim3(t()), 0, s, a);
+                                   dim3(threads), 0, s, a);
         });
     if (dW)
         hipLaunchKernelGGL(mx::column_sum, dim3((unsigned)(width / 32)), dim3(256), 0, s,

@@ -63,7 +63,8 @@ def _decode(fmt, q, s):
 
 # widths of every workgroup shape, its smallest and its largest row
 SHAPES = [(1, 32), (3, 96), (5, 512), (4, 544), (2, 2048), (3, 2080), (7, 4096), (2, 5120),
-          (3, 8192), (2, 8224), (1, 16384), (2, 16416), (1, 32768), (1, 32800), (2, 65536)]
+          (3, 8192), (2, 8224), (1, 16384), (2, 16416), (1, 32768), (1, 32800), (2, 65536),
+          (600, 32), (520, 1056), (514, 8192)]
 
 
 @pytest.mark.parametrize("residual", [False, True])

@@ -6,21 +6,20 @@
 
 namespace mx {
 
-// 1 / (1 + exp(-x)).  exp(-x) = 2^(-x log2 e), the product in two parts so
-// that its rounding does not grow with |x|; the hardware's exp2 and
-// reciprocal are good to one unit in the last place.  Arguments above 64
-// give 1 like 64 itself (an infinity would leave inf - inf in the low part);
-// below -87 the result, under 2^-125, counts as 0.  A NaN argument may give
-// a number: the callers multiply by the argument itself.
+// 1 / (1 + exp(-x)).  exp(-x) = 2^(-x log2 e): the product's rounding error
+// and the low part of log2 e are carried in `lo`, so that the error does not
+// grow with |x|; the hardware's exp2 and reciprocal are good to one unit in
+// the last place.  Arguments above 64 give 1 like 64 itself (an infinity
+// would leave inf - inf in the low part); below -87.3 exp(-x) passes 2^126 and
+// the result counts as 0.  A NaN argument may give a number: the callers
+// multiply by the argument itself.
 __device__ __forceinline__ float sigmoid(float x)
 {
     constexpr float L = -1.44269502162933349609f, L_LO = -1.925963e-8f;   // L + L_LO = -log2 e
     constexpr float LN2 = 0.693147180559945f;
-    const float c = __builtin_amdgcn_fmed3f(x, -88.f, 64.f);
+    const float c = fminf(x, 64.f);
     const float hi = c * L, lo = fmaf(c, L_LO, fmaf(c, L, -hi));
-    const float e = __builtin_amdgcn_exp2f(hi);
-    const float sig = __builtin_amdgcn_rcpf(1.f + fmaf(e, lo * LN2, e));
-    return x < -87.f ? 0.f : sig;
+    return __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_exp2f(hi), fmaf(lo, LN2, 1.f), 1.f));
 }
 
 }  // namespace mx

@@ -145,12 +145,13 @@ moe_sort(SortArgs a)
 // Rows of x (row_bytes each, and scale_bytes of scales) copied to the rows of
 // their pairs; rows of pairs without an expert are filled with zeros.  Each
 // token row is read once and written `top` times.  A wave takes 64 units of
-// U bytes of one token's row.
+// U bytes of a token's row (wave `seg` of the row's waves, the scales' after
+// the row's), for the tokens blockIdx.y, blockIdx.y + gridDim.y, ...
 struct GatherArgs {
     const uint8_t *x, *s;
     uint8_t *xs, *ss;
     const int32_t *row_of;
-    int64_t items, n, ldx, lds;                  // n: pairs; pitches in bytes
+    int64_t tokens, n, ldx, lds;                 // n: pairs; pitches in bytes
     int top, row_bytes, scale_bytes;
     int row_segs, segs;                          // waves per token: rows, and rows + scales
 };
@@ -171,20 +172,23 @@ __device__ __forceinline__ void gather_seg(const uint8_t *src, uint8_t *dst, int
         const int r = row_of[j];
         const int64_t to = r < 0 ? -1 - (int64_t)r : r;
         if (to >= n) continue;
-        *(T *)(dst + to * bytes + at) = r < 0 ? T{} : v;
+        __builtin_nontemporal_store(r < 0 ? T{} : v, (T *)(dst + to * bytes + at));
     }
 }
 
+// This wave's number among all waves along x.
+__device__ __forceinline__ int wave_x()
+{
+    return blockIdx.x * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
 template <int U, int US>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
 moe_gather(GatherArgs a)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t waves = (int64_t)gridDim.x * 4;
-    for (int64_t it = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-         it < a.items; it += waves) {
-        const int64_t t = it / a.segs;
-        const int seg = (int)(it - t * a.segs);
+    const int lane = threadIdx.x & 63, seg = wave_x();
+    if (seg >= a.segs) return;
+    for (int64_t t = blockIdx.y; t < a.tokens; t += gridDim.y) {
         const int32_t *row_of = a.row_of + t * a.top;
         if (seg < a.row_segs)
             gather_seg<U>(a.x + t * a.ldx, a.xs, a.row_bytes, (seg * 64 + lane) * U, row_of,
@@ -197,40 +201,51 @@ moe_gather(GatherArgs a)
 
 // out[t] = r[t] + sum over choices j, in order, of w[t][j] * y[row_of[t][j]];
 // pairs without an expert add nothing and nothing of theirs is read.  Without
-// weights each counts 1, which is the gradient of the gather.
+// weights each counts 1, which is the gradient of the gather.  A wave takes
+// 512 columns, four choices' loads at a time.
 struct CombineArgs {
     const void *y, *r;
     const float *w;
     const int32_t *row_of;
     void *out;
-    int64_t items, rows, ldy, ldr;               // rows of y; pitches in elements
-    int top, width, segs;
+    int64_t tokens, rows, ldy, ldr;              // rows of y; pitches in elements
+    int top, width;
 };
 
 template <int IN>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
 moe_combine(CombineArgs a)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t waves = (int64_t)gridDim.x * 4;
-    for (int64_t it = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-         it < a.items; it += waves) {
-        const int64_t t = it / a.segs;
-        const int col = ((int)(it - t * a.segs) * 64 + lane) * 8;
-        if (col >= a.width) continue;
+    const int col = (wave_x() * 64 + (threadIdx.x & 63)) * 8;
+    if (col >= a.width) return;
+    for (int64_t t = blockIdx.y; t < a.tokens; t += gridDim.y) {
+        const int32_t *row_of = a.row_of + t * a.top;
+        const float *w = a.w ? a.w + t * a.top : nullptr;
+        raw8<IN> rv;
+        if (a.r) rv = load8<IN, true>(a.r, t * a.ldr + col);
         float acc[8] = {};
-        for (int j = 0; j < a.top; ++j) {
-            const int r = a.row_of[t * a.top + j];
-            if (r < 0 || r >= a.rows) continue;
-            const float w = a.w ? a.w[t * a.top + j] : 1.f;
-            float v[8];
-            unpack8<IN>(load8<IN>(a.y, r * a.ldy + col), v);
+        for (int j0 = 0; j0 < a.top; j0 += 4) {
+            raw8<IN> yv[4];
+            bool live[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = fmaf(v[i], w, acc[i]);
+            for (int j = 0; j < 4; ++j) {
+                const int r = j0 + j < a.top ? row_of[j0 + j] : -1;
+                live[j] = r >= 0 && r < a.rows;
+                if (live[j]) yv[j] = load8<IN, true>(a.y, r * a.ldy + col);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (!live[j]) continue;
+                const float wj = w ? w[j0 + j] : 1.f;
+                float v[8];
+                unpack8<IN>(yv[j], v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] = fmaf(v[i], wj, acc[i]);
+            }
         }
         if (a.r) {
             float v[8];
-            unpack8<IN>(load8<IN>(a.r, t * a.ldr + col), v);
+            unpack8<IN>(rv, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] += v[i];
         }
@@ -240,46 +255,49 @@ moe_combine(CombineArgs a)
 
 // Gradient of the combination: dy[row_of[t][j]] = w[t][j] * dout[t] (zeros in
 // the rows of pairs without an expert) and dw[t][j] = <dout[t], y[row]> (0
-// without an expert).  A wave takes one pair at a time; the waves of a
-// workgroup share a token's dout row through the L1.
+// without an expert).  A wave takes one choice of a token, whole rows; the
+// waves of a workgroup share the token's dout row through the caches.
 struct CombineGradArgs {
     const void *dout, *y;
     const float *w;
     const int32_t *row_of;
     void *dy;
     float *dw;
-    int64_t n, rows, lddo, ldy;
+    int64_t tokens, rows, lddo, ldy;
     int top, width;
 };
 
 template <int IN>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
 moe_combine_grad(CombineGradArgs a)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t waves = (int64_t)gridDim.x * 4;
-    for (int64_t i = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-         i < a.n; i += waves) {
-        const int64_t t = i / a.top;
+    const int lane = threadIdx.x & 63, j = wave_x();
+    if (j >= a.top) return;
+    for (int64_t t = blockIdx.y; t < a.tokens; t += gridDim.y) {
+        const int64_t i = t * a.top + j;
         const int r = a.row_of[i];
         const int64_t to = r < 0 ? -1 - (int64_t)r : r;
-        const bool live = r >= 0 && to < a.rows;
-        const float w = live && a.w ? a.w[i] : 1.f;
         float dot = 0.f;
-        if (to < a.rows)
+        if (to >= a.rows) {
+            // a row that y leaves out: no expert
+        } else if (r < 0) {
+            for (int col = lane * 8; col < a.width; col += 512)
+                store8<IN>(a.dy, to * a.width + col, raw8<IN>{});
+        } else {
+            const float w = a.w[i];
+#pragma unroll 2
             for (int col = lane * 8; col < a.width; col += 512) {
-                float d[8] = {}, v[8];
-                if (live) {
-                    unpack8<IN>(load8<IN>(a.dout, t * a.lddo + col), d);
-                    unpack8<IN>(load8<IN>(a.y, to * a.ldy + col), v);
+                float d[8], v[8];
+                unpack8<IN>(load8<IN>(a.dout, t * a.lddo + col), d);
+                unpack8<IN>(load8<IN, true>(a.y, to * a.ldy + col), v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        dot = fmaf(d[e], v[e], dot);
-                        d[e] *= w;
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    dot = fmaf(d[e], v[e], dot);
+                    d[e] *= w;
                 }
                 store8<IN>(a.dy, to * a.width + col, pack8<IN>(d));
             }
+        }
         dot = wave_sum(dot);
         if (lane == 0) a.dw[i] = dot;
     }

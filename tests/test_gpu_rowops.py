@@ -8,7 +8,7 @@ Tolerances, in units u = 2^-24 of FP32 rounding:
   rstd, plus mean, eps, square root and quotient (4 u) and two products: 50 u.
 * norm gradient: 90 u of the row sum's terms, plus the outer arithmetic: 100 u
   of the sum of the terms' magnitudes; dw adds its rows one by one per
-  workgroup (rows / 512), then by 32 threads over 512 partial rows.
+  workgroup (rows / 256), then by 32 threads over 256 partial rows.
 * sigmoid: exp2 and reciprocal of 2 u each, their arguments 2 u, the sum and
   the products 1 u each: 10 u; the gradient's products 16 u of the magnitudes.
 * BF16 outputs: half a unit in the last place more."""
@@ -111,6 +111,48 @@ def test_norm_bf16_is_the_f32_norm_of_the_same_values(rows, width, fmt):
         assert torch.equal(o.q, p.q) and torch.equal(o.q_scale, p.q_scale)
 
 
+@pytest.mark.parametrize("fmt", FMTS, ids=FMT_IDS)
+def test_norm_quantizes_edge_values(fmt):
+    """Rows of ones with eps 0 have rstd 1, so y is the weights exactly: every
+    element value, midpoint and value next to overflow, at block scales from
+    the smallest subnormals to the largest finite values, both signs, zeros;
+    and overflowing residual sums round to infinities."""
+    torch = _torch()
+    log("norm edge values fmt %d" % fmt)
+    top = {mxg.FMT_E2M1: 6.0, mxg.FMT_E4M3: 448.0, mxg.FMT_E5M2: 57344.0, mxg.FMT_E2M3: 7.5,
+           mxg.FMT_E3M2: 28.0}[fmt]
+    # every code of the format, in whole rows of bytes
+    codes = torch.arange(768, dtype=torch.int64).remainder(256).to(torch.uint8)
+    values = {mxg.FMT_E2M1: 64, mxg.FMT_E4M3: 32, mxg.FMT_E5M2: 32}.get(fmt, 128)
+    row = {mxg.FMT_E2M1: 32, mxg.FMT_E4M3: 32, mxg.FMT_E5M2: 32}.get(fmt, 96)
+    grid = _decode(fmt, codes.view(-1, row), torch.full((768 // row, values // 32), 127,
+                                                        dtype=torch.uint8))
+    g = np.unique(np.abs(grid[np.isfinite(grid)]))
+    mids = (g[1:] + g[:-1]) / 2
+    over = top * (1 + np.arange(1, 9) / 32.0)
+    vals = np.concatenate([g, mids, mids * (1 + 2.0 ** -22), mids * (1 - 2.0 ** -22), over, [0.0]])
+    vals = np.concatenate([vals, -vals])
+    vals = np.concatenate([vals, np.zeros(-len(vals) % 31)]).reshape(-1, 31)
+    rows = []
+    for e in (0, -3, 40, 100, -60, -100, -118, -126, -132, -140, -149):
+        block = np.concatenate([np.full((len(vals), 1), top), vals], 1) / top * 2.0 ** e
+        rows.append(block.reshape(-1))
+    w = np.concatenate(rows + [np.zeros(32), np.full(32, 3.0e38), np.full(32, -1e-45)])
+    w = w.astype(np.float32)
+    for at in range(0, len(w), 65536):
+        part = w[at:at + 65536]
+        o = mxg.mx_rmsnorm_quantize(torch.ones((2, len(part)), device="cuda"), _dev(part), fmt,
+                                    eps=0.0, need_y=True)
+        assert (_h64(o.y) == part.astype(np.float64)).all()
+        rq, rs = oracle.quantize(fmt, np.stack([part, part]).astype(np.float64))
+        assert (o.q_scale.cpu().numpy() == rs).all() and (o.q.cpu().numpy() == rq).all()
+    big = torch.tensor([[3.3895313892515355e38] * 32], device="cuda").to(torch.bfloat16)
+    more = torch.full_like(big, 6.7e35)
+    o = mxg.mx_rmsnorm_quantize(big, torch.ones(32, device="cuda"), fmt, residual=more)
+    want = (big.float() + more.float()).to(torch.bfloat16)
+    assert torch.isinf(want).all() and torch.equal(o.h, want)
+
+
 def test_norm_pitches_streams_and_single_outputs():
     torch = _torch()
     log("norm pitches")
@@ -175,7 +217,7 @@ def test_norm_gradient(rows, width, dtype):
         want, want_dw, mag, mag_dw = ref.norm_grad(_h64(dy), _h64(h), _h64(w), eps, extra)
         # rstd is itself 50 u off, and appears up to three times in a term
         assert (abs(_h64(got) - want) <= 250 * U * mag + half * abs(want)).all()
-    depth = rows / 512 + 1 + 16 + 32 + 55
+    depth = rows / 256 + 1 + 16 + 32 + 55
     assert (abs(_h64(dw) - want_dw) <= depth * U * mag_dw).all()
 
 

@@ -65,12 +65,14 @@ def declare(L):
 
 
 _torch_module = None
+_codes = {}             # torch dtype -> MX_IN_* code
 
 
 def _torch():
     global _torch_module
     if _torch_module is None:
         import torch
+        _codes.update({torch.float32: _m.IN_FP32, torch.bfloat16: _m.IN_BF16})
         _torch_module = torch
     return _torch_module
 
@@ -93,18 +95,11 @@ def _enter(device, stream):
     return _HERE, current or None
 
 
-def _check(rc):
-    if rc != _m.MX_OK:
-        _m._raise(rc)
-
-
 def _dtype_code(t, name):
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return _m.IN_BF16
-    if t.dtype == torch.float32:
-        return _m.IN_FP32
-    raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    return code
 
 
 def _tensor(t, name, device=None):
@@ -178,6 +173,7 @@ def mx_rmsnorm_quantize(x, weight, fmt, residual=None, eps=1e-6, need_y=False, n
     ldr = 0
     if residual is not None:
         ldr = _rows(residual, "residual", width, rows, x.dtype, dev)
+    L = _m.lib()
     ctx, s = _enter(dev, stream)
     with ctx:
         h = x if residual is None else x.new_empty((rows, width))
@@ -189,10 +185,12 @@ def mx_rmsnorm_quantize(x, weight, fmt, residual=None, eps=1e-6, need_y=False, n
             y = x.new_empty((rows, width))
         if need_rstd:
             rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        _check(_m.lib().mx_rmsnorm_quantize(
+        rc = L.mx_rmsnorm_quantize(
             fmt or 0, code, _dtype_code(weight, "weight"), rows, width, x.data_ptr(), ldx,
             _ptr(residual), ldr, weight.data_ptr(), eps, h.data_ptr(), _ptr(y), _ptr(q), _ptr(qs),
-            _ptr(rstd), s))
+            _ptr(rstd), s)
+    if rc:
+        _m._raise(rc)
     return NormOut(q, qs, h, y, rstd)
 
 
@@ -222,10 +220,12 @@ def mx_rmsnorm_backward(dy, h, rstd, weight, dh=None, need_dw=True, stream=None)
                 _m._raise(nbytes)
             dw = torch.empty(width, dtype=torch.float32, device=dev)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _check(L.mx_rmsnorm_backward(
+        rc = L.mx_rmsnorm_backward(
             code, _dtype_code(weight, "weight"), rows, width, dy.data_ptr(), lddy, h.data_ptr(),
             ldh, rstd.data_ptr(), weight.data_ptr(), _ptr(dh), lddh, dx.data_ptr(), _ptr(dw),
-            _ptr(ws), nbytes, s))
+            _ptr(ws), nbytes, s)
+    if rc:
+        _m._raise(rc)
     return dx, dw
 
 
@@ -240,12 +240,15 @@ def mx_swiglu_quantize(gate_up, fmt, stream=None):
     width = two // 2
     dev = gate_up.device
     code = _dtype_code(gate_up, "gate_up")
+    L = _m.lib()
     ctx, s = _enter(dev, stream)
     with ctx:
         q = torch.empty((rows, _m._row_bytes(_fmt(fmt), width)), dtype=torch.uint8, device=dev)
         qs = torch.empty((rows, width // 32), dtype=torch.uint8, device=dev)
-        _check(_m.lib().mx_swiglu_quantize(fmt, code, rows, width, gate_up.data_ptr(), ld,
-                                           q.data_ptr(), qs.data_ptr(), s))
+        rc = L.mx_swiglu_quantize(fmt, code, rows, width, gate_up.data_ptr(), ld,
+                                           q.data_ptr(), qs.data_ptr(), s)
+    if rc:
+        _m._raise(rc)
     return q, qs
 
 
@@ -260,11 +263,14 @@ def mx_swiglu_backward(dy, gate_up, stream=None):
     dev = gate_up.device
     code = _dtype_code(gate_up, "gate_up")
     lddy = _rows(dy, "dy", two // 2, rows, gate_up.dtype, dev)
+    L = _m.lib()
     ctx, s = _enter(dev, stream)
     with ctx:
         dgu = gate_up.new_empty((rows, two))
-        _check(_m.lib().mx_swiglu_backward(code, rows, two // 2, dy.data_ptr(), lddy,
-                                           gate_up.data_ptr(), ld, dgu.data_ptr(), s))
+        rc = L.mx_swiglu_backward(code, rows, two // 2, dy.data_ptr(), lddy,
+                                           gate_up.data_ptr(), ld, dgu.data_ptr(), s)
+    if rc:
+        _m._raise(rc)
     return dgu
 
 
@@ -291,8 +297,10 @@ def mx_moe_sort(ids, experts, stream=None):
         group_rows = torch.empty(experts, dtype=torch.int64, device=dev)
         row_of = torch.empty((tokens, top), dtype=torch.int32, device=dev)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        _check(L.mx_moe_sort(ids.element_size(), tokens, top, experts, ids.data_ptr(),
-                             group_rows.data_ptr(), row_of.data_ptr(), _ptr(ws), nbytes, s))
+        rc = L.mx_moe_sort(ids.element_size(), tokens, top, experts, ids.data_ptr(),
+                             group_rows.data_ptr(), row_of.data_ptr(), _ptr(ws), nbytes, s)
+    if rc:
+        _m._raise(rc)
     return MoePlan(group_rows, row_of)
 
 
@@ -320,15 +328,18 @@ def mx_moe_gather(plan, x, x_scale=None, stream=None):
         ssize = x_scale.element_size()
         lds = _rows(x_scale, "x_scale", rows=tokens, device=dev) * ssize
         sbytes = x_scale.shape[1] * ssize
+    L = _m.lib()
     ctx, s = _enter(dev, stream)
     with ctx:
         xs = x.new_empty((tokens * top, x.shape[1]))
         ss = None
         if x_scale is not None:
             ss = x_scale.new_empty((tokens * top, x_scale.shape[1]))
-        _check(_m.lib().mx_moe_gather(tokens, top, row_of.data_ptr(), x.data_ptr(),
+        rc = L.mx_moe_gather(tokens, top, row_of.data_ptr(), x.data_ptr(),
                                       x.shape[1] * size, ld * size, _ptr(x_scale), sbytes, lds,
-                                      xs.data_ptr(), _ptr(ss), s))
+                                      xs.data_ptr(), _ptr(ss), s)
+    if rc:
+        _m._raise(rc)
     return xs, ss
 
 
@@ -356,12 +367,15 @@ def mx_moe_combine(plan, y, weights=None, residual=None, stream=None):
     if weights is not None:
         _weights(weights, row_of, dev)
     ldr = 0 if residual is None else _rows(residual, "residual", width, tokens, y.dtype, dev)
+    L = _m.lib()
     ctx, s = _enter(dev, stream)
     with ctx:
         out = y.new_empty((tokens, width))
-        _check(_m.lib().mx_moe_combine(code, tokens, top, width, row_of.data_ptr(), y.data_ptr(),
+        rc = L.mx_moe_combine(code, tokens, top, width, row_of.data_ptr(), y.data_ptr(),
                                        y.shape[0], ldy, _ptr(weights), _ptr(residual), ldr,
-                                       out.data_ptr(), s))
+                                       out.data_ptr(), s)
+    if rc:
+        _m._raise(rc)
     return out
 
 
@@ -378,13 +392,16 @@ def mx_moe_combine_backward(plan, dout, y, weights, stream=None):
     width = y.shape[1]
     lddo = _rows(dout, "dout", width, tokens, y.dtype, dev)
     _weights(weights, row_of, dev)
+    L = _m.lib()
     ctx, s = _enter(dev, stream)
     with ctx:
         dy = y.new_empty((y.shape[0], width))
         dw = torch.empty((tokens, top), dtype=torch.float32, device=dev)
-        _check(_m.lib().mx_moe_combine_backward(
+        rc = L.mx_moe_combine_backward(
             code, tokens, top, width, row_of.data_ptr(), dout.data_ptr(), lddo, y.data_ptr(),
-            y.shape[0], ldy, weights.data_ptr(), dy.data_ptr(), dw.data_ptr(), s))
+            y.shape[0], ldy, weights.data_ptr(), dy.data_ptr(), dw.data_ptr(), s)
+    if rc:
+        _m._raise(rc)
     return dy, dw
 
 
@@ -428,14 +445,17 @@ def mx_gemm_fused(a, a_scale, b, b_scale, fmt, bias=None, act=ACT_NONE, residual
         if t.device != dev:
             raise ValueError("all operands must be on the same device")
     bias_code, ldr = _epilogue(M, N, tdt, dev, bias, residual, out)
+    L = _m.lib()
     ctx, s = _enter(dev, stream)
     with ctx:
         if out is None:
             out = torch.empty((M, N), dtype=tdt, device=dev)
-        _check(_m.lib().mx_gemm_fused(
+        rc = L.mx_gemm_fused(
             fmt, fmt_b, M, N, K, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
             b_scale.data_ptr(), _ptr(bias), bias_code, act, _ptr(residual), ldr, out.data_ptr(),
-            code, s))
+            code, s)
+    if rc:
+        _m._raise(rc)
     return out
 
 
@@ -453,11 +473,14 @@ def mx_gemm_bf16_fused(a, b, bias=None, act=ACT_NONE, residual=None, out_dtype=N
     if b.device != dev:
         raise ValueError("all operands must be on the same device")
     bias_code, ldr = _epilogue(M, N, tdt, dev, bias, residual, out)
+    L = _m.lib()
     ctx, s = _enter(dev, stream)
     with ctx:
         if out is None:
             out = torch.empty((M, N), dtype=tdt, device=dev)
-        _check(_m.lib().mx_gemm_bf16_fused(M, N, K, a.data_ptr(), b.data_ptr(), _ptr(bias),
+        rc = L.mx_gemm_bf16_fused(M, N, K, a.data_ptr(), b.data_ptr(), _ptr(bias),
                                            bias_code, act, _ptr(residual), ldr, out.data_ptr(),
-                                           code, s))
+                                           code, s)
+    if rc:
+        _m._raise(rc)
     return out

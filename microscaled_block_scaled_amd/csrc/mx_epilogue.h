@@ -135,8 +135,7 @@ __device__ __forceinline__ void fused_band(const EP &ep, uint8_t *stage, void *C
         } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                w[q] = (int)((uint32_t)f32_to_bf16(v[2 * q]) |
-                             ((uint32_t)f32_to_bf16(v[2 * q + 1]) << 16));
+                w[q] = (int)bf16_pair(v[2 * q], v[2 * q + 1]);
         }
         otype *dst = (otype *)C + (int64_t)row * N + col;
         if (vec_c) {                                            // N % VE == 0: whole chunks

@@ -63,8 +63,7 @@ __device__ __forceinline__ raw8<IN> pack8(const float (&v)[8])
             r.q[0][i] = __float_as_int(v[i]);
             r.q[1][i] = __float_as_int(v[4 + i]);
         } else {
-            r.q[0][i] = (int)((uint32_t)f32_to_bf16(v[2 * i]) |
-                              ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16));
+            r.q[0][i] = (int)bf16_pair(v[2 * i], v[2 * i + 1]);
         }
     }
     return r;

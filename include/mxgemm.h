@@ -470,7 +470,8 @@ int mx_hbm_read_ceiling(const void *src, int64_t bytes, uint32_t *out, void *str
  *   - errors, asynchrony and determinism are as for mx_gemm.  An output
  *     overlaps no input unless it says otherwise.  They allocate nothing and
  *     can be captured in a graph; where a workspace is needed it is the
- *     caller's, used on `stream` until the call's work is done there.
+ *     caller's, used on `stream` until the call's work is done there (the
+ *     fused products use the library's own, as mx_gemm does).
  */
 
 /* Longest row of a row operator. */
@@ -599,9 +600,8 @@ int mx_moe_combine_backward(int dtype, int64_t tokens, int64_t top, int64_t widt
 enum { MX_ACT_NONE = 0, MX_ACT_RELU = 1, MX_ACT_SILU = 2, MX_ACT_GELU = 3, MX_ACT_GELU_TANH = 4 };
 
 /*
- * C = residual + act(A * B^T + bias): mx_gemm_mixed (its plan's choice) with
- * bias, activation and residual applied to the FP32 sums before C's one
- * rounding.
+ * C = residual + act(A * B^T + bias): mx_gemm_mixed's product with bias,
+ * activation and residual applied to the FP32 sums before C's one rounding.
  *   fmt_a,
  *   fmt_b      E2M1 with E2M1, E4M3 with E4M3, or E4M3 with E2M1;
  *              MX_ERR_FORMAT otherwise
@@ -609,17 +609,27 @@ enum { MX_ACT_NONE = 0, MX_ACT_RELU = 1, MX_ACT_SILU = 2, MX_ACT_GELU = 3, MX_AC
  *   act        MX_ACT_*
  *   residual   M x N in C's type with pitch ldr, 16-byte aligned, or NULL;
  *              may be C itself (with ldr == N)
- * Everything else as for mx_gemm.
+ * Everything else as for mx_gemm (with a split K, its per-stream workspace).
  */
 int mx_gemm_fused(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, const void *A,
                   const void *A_scale, const void *B, const void *B_scale, const void *bias,
                   int bias_dtype, int act, const void *residual, int64_t ldr, void *C,
                   int out_dtype, void *stream);
 
-/* The same on mx_gemm_bf16. */
+/* The same on mx_gemm_bf16's operands. */
 int mx_gemm_bf16_fused(int64_t M, int64_t N, int64_t K, const void *A, const void *B,
                        const void *bias, int bias_dtype, int act, const void *residual,
                        int64_t ldr, void *C, int out_dtype, void *stream);
+
+/*
+ * The launch they would make: the decode kernel or a tile (128 x 64 and
+ * 64 x 64 among them, so that products of a few hundred rows fill the GPU)
+ * and a K split.  Host logic only; returns MX_OK or their argument error
+ * (MX_ERR_NULL for a NULL plan).
+ */
+int mx_gemm_fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, int out_dtype,
+                       mx_plan_t *plan);
+int mx_gemm_bf16_fused_plan(int64_t M, int64_t N, int64_t K, int out_dtype, mx_plan_t *plan);
 
 #ifdef __cplusplus
 }

@@ -585,4 +585,4 @@ from .block import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU,  # no
                     MOE_MAX_TOP, ROW_MAX_WIDTH, MoePlan, NormOut, mx_gemm_bf16_fused,
                     mx_gemm_fused, mx_moe_combine, mx_moe_combine_backward, mx_moe_gather,
                     mx_moe_sort, mx_rmsnorm_backward, mx_rmsnorm_quantize, mx_swiglu_backward,
-                    mx_swiglu_quantize)
+                    mx_swiglu_quantize, plan_fused)

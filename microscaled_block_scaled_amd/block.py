@@ -59,7 +59,9 @@ def declare(L):
                                              vp, vp]),
             ("mx_gemm_fused", ci, [ci, ci, i64, i64, i64, vp, vp, vp, vp, vp, ci, ci, vp, i64, vp,
                                    ci, vp]),
-            ("mx_gemm_bf16_fused", ci, [i64, i64, i64, vp, vp, vp, ci, ci, vp, i64, vp, ci, vp])):
+            ("mx_gemm_bf16_fused", ci, [i64, i64, i64, vp, vp, vp, ci, ci, vp, i64, vp, ci, vp]),
+            ("mx_gemm_fused_plan", ci, [ci, ci, i64, i64, i64, ci, vp]),
+            ("mx_gemm_bf16_fused_plan", ci, [i64, i64, i64, ci, vp])):
         f = getattr(L, name)
         f.restype, f.argtypes = res, args
 
@@ -403,6 +405,21 @@ def mx_moe_combine_backward(plan, dout, y, weights, stream=None):
     if rc:
         _m._raise(rc)
     return dy, dw
+
+
+def plan_fused(fmt, M, N, K, out_dtype=None, fmt_b=None):
+    """How mx_gemm_fused would run this problem (a dict), or with ``fmt`` None
+    mx_gemm_bf16_fused; host logic only."""
+    p = _m.MxPlan()
+    out = _m.OUT_BF16 if out_dtype is None else int(out_dtype)
+    if fmt is None:
+        rc = _m.lib().mx_gemm_bf16_fused_plan(M, N, K, out, ctypes.addressof(p))
+    else:
+        rc = _m.lib().mx_gemm_fused_plan(fmt, fmt if fmt_b is None else fmt_b, M, N, K, out,
+                                         ctypes.addressof(p))
+    if rc:
+        _m._raise(rc)
+    return p.as_dict()
 
 
 def _epilogue(M, N, tdt, dev, bias, residual, out):

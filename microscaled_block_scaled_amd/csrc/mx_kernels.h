@@ -246,10 +246,15 @@ struct NoGroups {
     static constexpr bool grouped = false;
 };
 
-// A GEMM without a fused epilogue writes its sums as they are (the fused one
-// is struct Epilogue of mx_epilogue.h).
+// What the sums of a GEMM become.  NoEpilogue writes them as they are (the
+// fused epilogue is struct Epilogue of mx_epilogue.h).  stream_b: the short
+// tiles read B with the nontemporal hint.
 struct NoEpilogue {
-    static constexpr bool fused = false;
+    static constexpr bool fused = false, stream_b = true;
+};
+// NoEpilogue without that hint: the split-K slices of the fused GEMMs.
+struct PlainSums {
+    static constexpr bool fused = false, stream_b = false;
 };
 template <typename EP> __device__ float bias_at(const EP &ep, int n);
 template <int OUT, typename EP>
@@ -419,8 +424,9 @@ tile_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
     const uint32_t ext_b = whole_b ? 0xffffffffu : (uint32_t)((last_b + 1) * rowbb - kboffb);
     // B is streamed once per tile when every tile column has a single row
     // tile (the short tiles serve M <= their height): it takes the
-    // nontemporal hint there.
-    constexpr int AUXB = BM <= 128 ? kStream : 0;
+    // nontemporal hint there (not in the fused GEMMs, whose short tiles serve
+    // any M).
+    constexpr int AUXB = BM <= 128 && EP::stream_b ? kStream : 0;
     // Per operand (slab row bytes R, rows per copy instruction 1024/R): lane
     // l copies chunk l % (R/16) of row l / (R/16) of a block of rows, into
     // LDS chunk cpc of that row, which holds global chunk cpc ^ swz(row).

@@ -30,30 +30,45 @@ void go_cfg(const void *A, const void *As, const void *B, const void *Bs, void *
     }
     // the slices' sums as they are, then the epilogue where they are added
     const int64_t plane = plane_of(M, N);
-    hipLaunchKernelGGL((mx::tile_kernel<FA, FB, mx::OF32, BM, BN, WGM, WGN, S>), grid, block, 0,
-                       s, a, as, b, bs, (void *)W, (int)M, (int)N, (int)K, tiles_m, tiles_n, gm,
-                       (int)slice_k(K, split), plane);
+    hipLaunchKernelGGL((mx::tile_kernel<FA, FB, mx::OF32, BM, BN, WGM, WGN, S, mx::NoGroups,
+                                        mx::PlainSums>),
+                       grid, block, 0, s, a, as, b, bs, (void *)W, (int)M, (int)N, (int)K,
+                       tiles_m, tiles_n, gm, (int)slice_k(K, split), plane, mx::NoGroups{},
+                       mx::PlainSums{});
     hipLaunchKernelGGL((mx::splitk_fused<OUT>), dim3((unsigned)cdiv(M * N, 1024)), dim3(256), 0,
                        s, (const float *)W, C, (int)(M * N), (int)N, plane, split, ep);
 }
+
+// The tiles of the fused GEMMs: {BM, BN, waves along M, waves along N}, and
+// the cost of one tile of theirs in units of a 64 x 64 tile's.  The small
+// tiles are for the many products of a block that the 256-row tiles cannot
+// spread over the GPU (2944 columns and 257 rows: 46 workgroups of 256 x 128).
+struct FusedTile { int bm, bn, wgm, wgn; double cost; };
+constexpr FusedTile kFusedTiles[] = {
+    {256, 256, 4, 2, 6.0}, {256, 192, 4, 2, 5.3}, {256, 128, 4, 2, 3.9},
+    {128, 128, 4, 2, 2.4}, {128, 64, 2, 2, 1.6}, {64, 64, 2, 2, 1.0},
+};
 
 template <int FA, int FB, int OUT>
 bool go_tile(const mx_plan_t &p, const void *A, const void *As, const void *B, const void *Bs,
              void *C, int64_t M, int64_t N, int64_t K, float *W, const mx::Epilogue &ep,
              hipStream_t s)
 {
+    // The smallest tile takes the deepest ring that lets two workgroups share
+    // a CU: 4 slabs, or 3 where the scale period allows no more (E2M1).
+    constexpr int S64 = FA == mx::FP4 ? 3 : 4;
 #define MX_CFG(BM_, BN_, WM_, WN_, S_)                                                     \
-    if (p.tile_m == BM_ && p.tile_n == BN_ && p.threads == WM_ * WN_ * 64) {              \
+    if (p.tile_m == BM_ && p.tile_n == BN_) {                                              \
         go_cfg<FA, FB, OUT, BM_, BN_, WM_, WN_, S_>(A, As, B, Bs, C, M, N, K, p.split_k,   \
                                                     W, ep, s);                             \
         return true;                                                                       \
     }
     MX_CFG(256, 256, 4, 2, 2)
     MX_CFG(256, 192, 4, 2, 2)
-    MX_CFG(256, 160, 4, 1, 2)
     MX_CFG(256, 128, 4, 2, 3)
-    MX_CFG(128, 128, 2, 2, 3)
-    MX_CFG(64, 256, 1, 8, 3)
+    MX_CFG(128, 128, 4, 2, 3)
+    MX_CFG(128, 64, 2, 2, 3)
+    MX_CFG(64, 64, 2, 2, S64)
 #undef MX_CFG
     return false;
 }
@@ -97,6 +112,46 @@ bool fused_pair(int fmt_a, int fmt_b)
            (fmt_a == MX_FMT_E4M3 && fmt_b == MX_FMT_E4M3) ||
            (fmt_a == MX_FMT_E4M3 && fmt_b == MX_FMT_E2M1) ||
            (fmt_a == kFmtBF16 && fmt_b == kFmtBF16);
+}
+
+// The tile and split with the least estimated time.  A CU works through its
+// share of the tiles, so the tiles cost ceil(tiles / CUs) * cost per K-value,
+// and splitting K adds a second kernel and a round trip of the planes.  The
+// costs per tile and the two constants were fitted to times of all tiles and
+// splits over 51 shapes (M 20 .. 2048, N 1000 .. 28672, K 1024 .. 28672, each
+// with bias and residual, operands rotating) in E4M3, E2M1, E4M3 x E2M1 and
+// BF16 on MI355X: the choice takes 1.02 times the best tile and split's time
+// (geometric mean; worst 1.26), the unfused plan's choice 1.55 times (worst
+// 3.1).  In E4M3 293 x 3443 x 2688 takes 13 us against 26, 453 x 1628 x 1664
+// 7.8 against 18.6.
+void fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, mx_plan_t *p)
+{
+    // microseconds of a 64 x 64 tile per 128 K-values
+    const double unit = fmt_a == kFmtBF16 ? 0.45 : fmt_a == MX_FMT_E2M1 ? 0.16
+                      : fmt_b == MX_FMT_E2M1 ? 0.20 : 0.25;
+    double best = -1.0;
+    memset(p, 0, sizeof(*p));
+    for (const FusedTile &c : kFusedTiles) {
+        const int64_t tiles = cdiv(M, c.bm) * cdiv(N, c.bn);
+        for (int req = 1; req <= MX_MAX_SPLIT_K; req *= 2) {
+            const int64_t k = slice_k(K, req);
+            const int split = req == 1 ? 1 : (int)cdiv(K, k);
+            // slices of at least 1024 K, planes and grid within 32-bit indices
+            if (req > 1 && (split < 2 || k < 1024 || M * N >= ((int64_t)1 << 30))) break;
+            double t = (double)cdiv(tiles * split, kCUs) * c.cost * unit *
+                       (double)(split > 1 ? k : K) / 128.0;
+            if (split > 1) t += 3.5 + 2.3e-6 * (double)(M * N * split);
+            if (best >= 0.0 && t >= best) continue;
+            best = t;
+            p->variant = MX_VARIANT_TILE;
+            p->tile_m = c.bm;
+            p->tile_n = c.bn;
+            p->split_k = split;
+            p->threads = c.wgm * c.wgn * 64;
+            p->workgroups = tiles * split;
+            p->workspace_bytes = split > 1 ? split * plane_of(M, N) * 4 : 0;
+        }
+    }
 }
 
 bool launch_fused(int fmt_a, int fmt_b, const mx_plan_t &p, int out_dtype, const void *A,

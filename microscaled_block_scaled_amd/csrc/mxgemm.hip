@@ -478,22 +478,43 @@ int check_epilogue(int64_t N, int out_dtype, const void *bias, int bias_dtype, i
 
 }  // namespace
 
+extern "C" int mx_gemm_fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K,
+                                  int out_dtype, mx_plan_t *plan)
+{
+    if (!plan) return MX_ERR_NULL;
+    const int rc = check_args(fmt_a, M, N, K, out_dtype);
+    if (rc != MX_OK) return rc;
+    if (!fused_pair(fmt_a, fmt_b)) return MX_ERR_FORMAT;
+    const bool wide = fmt_b == MX_FMT_E2M1 && fmt_a == MX_FMT_E4M3;
+    if (decode_fits(fmt_a, fmt_b, M, N, K) && decode_preferred(M, N, K, wide))
+        fill_decode_plan(N, plan);
+    else
+        fused_plan(fmt_a, fmt_b, M, N, K, plan);
+    return plan->workgroups > kMaxGrid ? MX_ERR_SHAPE : MX_OK;
+}
+
+extern "C" int mx_gemm_bf16_fused_plan(int64_t M, int64_t N, int64_t K, int out_dtype,
+                                       mx_plan_t *plan)
+{
+    if (!plan) return MX_ERR_NULL;
+    const int rc = check_args_bf16(M, N, K, out_dtype);
+    if (rc != MX_OK) return rc;
+    fused_plan(kFmtBF16, kFmtBF16, M, N, K, plan);
+    return plan->workgroups > kMaxGrid ? MX_ERR_SHAPE : MX_OK;
+}
+
 extern "C" int mx_gemm_fused(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K,
                              const void *A, const void *A_scale, const void *B,
                              const void *B_scale, const void *bias, int bias_dtype, int act,
                              const void *residual, int64_t ldr, void *C, int out_dtype,
                              void *stream)
 {
-    int rc = check_args(fmt_a, M, N, K, out_dtype);
+    mx_plan_t plan;
+    int rc = mx_gemm_fused_plan(fmt_a, fmt_b, M, N, K, out_dtype, &plan);
     if (rc != MX_OK) return rc;
-    if (fmt_b < MX_FMT_E2M1 || fmt_b > MX_FMT_E3M2 || !fused_pair(fmt_a, fmt_b))
-        return MX_ERR_FORMAT;
     mx::Epilogue ep;
     rc = check_epilogue(N, out_dtype, bias, bias_dtype, act, residual, ldr, &ep);
     if (rc != MX_OK) return rc;
-    mx_plan_t plan;
-    plan_for(fmt_a, fmt_b, M, N, K, &plan);
-    if (plan.workgroups > kMaxGrid) return MX_ERR_SHAPE;
     return run_plan(plan, fmt_a, fmt_b, M, N, K, A, A_scale, B, B_scale, C, out_dtype, stream,
                     false, &ep);
 }
@@ -503,14 +524,12 @@ extern "C" int mx_gemm_bf16_fused(int64_t M, int64_t N, int64_t K, const void *A
                                   const void *residual, int64_t ldr, void *C, int out_dtype,
                                   void *stream)
 {
-    int rc = check_args_bf16(M, N, K, out_dtype);
+    mx_plan_t plan;
+    int rc = mx_gemm_bf16_fused_plan(M, N, K, out_dtype, &plan);
     if (rc != MX_OK) return rc;
     mx::Epilogue ep;
     rc = check_epilogue(N, out_dtype, bias, bias_dtype, act, residual, ldr, &ep);
     if (rc != MX_OK) return rc;
-    mx_plan_t plan;
-    fill_plan(choose_tile(M, N, K), M, N, K, &plan);
-    if (plan.workgroups > kMaxGrid) return MX_ERR_SHAPE;
     return run_plan(plan, kFmtBF16, kFmtBF16, M, N, K, A, nullptr, B, nullptr, C, out_dtype,
                     stream, false, &ep);
 }

@@ -156,6 +156,37 @@ def test_fused(over, code):
         assert _call("mx_gemm_bf16_fused", bf, over) == code
 
 
+def test_fused_plans():
+    """Every plan is a kernel that is compiled, covers C, and splits K into at
+    most MAX_SPLIT_K slices with planes for each; huge problems are refused."""
+    tiles = {(256, 256): 512, (256, 192): 512, (256, 128): 512, (128, 128): 512, (128, 64): 256,
+             (64, 64): 256}
+    for fmt, fmt_b in ((1, 1), (2, 2), (2, 1), (None, None)):
+        for M in (1, 31, 33, 64, 65, 300, 2048, 100000, 1 << 30):
+            for N in (1, 64, 1000, 8192, 1 << 20):
+                for K in (128, 512, 640, 4096, 28672, 1 << 20):
+                    try:
+                        p = mxg.plan_fused(fmt, M, N, K, fmt_b=fmt_b)
+                    except ValueError:
+                        assert M * N >= 1 << 43
+                        continue
+                    if p["variant"] == mxg.VARIANT_DECODE:
+                        assert fmt is not None and M <= 32 and K >= 512
+                        continue
+                    bm, bn = p["tile_m"], p["tile_n"]
+                    assert tiles[bm, bn] == p["threads"]
+                    assert p["workgroups"] == -(-M // bm) * -(-N // bn) * p["split_k"]
+                    assert 1 <= p["split_k"] <= mxg.MAX_SPLIT_K and (p["split_k"] == 1 or K >= 2048)
+                    need = p["split_k"] * -(-M * N // 64) * 256 if p["split_k"] > 1 else 0
+                    assert p["workspace_bytes"] == need
+    with pytest.raises(ValueError):
+        mxg.plan_fused(3, 8, 64, 512)
+    with pytest.raises(ValueError):
+        mxg.plan_fused(None, 8, 64, 20)
+    assert mxg.lib().mx_gemm_fused_plan(2, 2, 8, 64, 512, 2, None) == mxg.MX_ERR_NULL
+    assert mxg.lib().mx_gemm_bf16_fused_plan(8, 64, 512, 2, None) == mxg.MX_ERR_NULL
+
+
 def test_workspaces():
     L = mxg.lib()
     assert L.mx_rmsnorm_backward_workspace(0, 64) == 0

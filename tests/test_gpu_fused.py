@@ -1,8 +1,8 @@
 """GPU tests of the products with a fused epilogue, C = residual +
 act(A * B^T + bias), on every kernel a plan can choose (decode, tiles, split-K).
 
-With nothing to fuse the result is mx_gemm's, bit for bit.  Otherwise it is
-held to the 64-bit result within: the product's own bound (1e-5 T, and the
+With nothing to fuse and no K split the result is mx_gemm's, bit for bit, on
+the same kernel or another tile.  Otherwise it is held to the 64-bit result within: the product's own bound (1e-5 T, and the
 oracle's term E for 8-bit operands), which an activation's slope (below 1.13)
 carries on; 16 units u = 2^-24 of the activation's value and argument; two
 units for the sums with bias and residual; half a unit in the last place of
@@ -28,7 +28,9 @@ PAIR_IDS = ["e4m3", "e2m1", "w4a8", "bf16"]
 # split-K: few tiles and a long K
 SHAPES = [(1, 64, 512), (8, 1000, 1024), (9, 33, 512), (16, 40, 640), (32, 257, 512),
           (1, 7, 128), (33, 520, 256), (64, 257, 384), (100, 130, 256), (130, 264, 384),
-          (300, 1000, 256), (256, 2048, 128), (70, 512, 8192), (200, 130, 4096)]
+          (300, 1000, 256), (256, 2048, 128), (70, 512, 8192), (200, 130, 4096),
+          (520, 2052, 384), (700, 4102, 256), (1030, 4097, 128), (2000, 6144, 128),
+          (1500, 7000, 128), (2040, 8100, 128)]
 
 
 def _torch():
@@ -92,8 +94,13 @@ def test_against_the_oracle(pair, M, N, K):
         resw[:, :N] = res
         bias = torch.from_numpy(bias32).float().cuda()
         log("fused %s %dx%dx%d %s" % (pair, M, N, K, out_dtype))
-        plain = _plain(pair, dev, out_dtype=out_dtype)
-        assert torch.equal(_fused(pair, dev, out_dtype=out_dtype), plain)
+        plan = mxg.plan_fused(None if pair is None else pair[0], M, N, K,
+                              fmt_b=None if pair is None else pair[1])
+        if plan["split_k"] == 1:
+            dec = plan["variant"] == mxg.VARIANT_DECODE
+            plain = _plain(pair, dev, out_dtype=out_dtype,
+                           tile=(32, 32) if dec else (256, 128), split_k=1)
+            assert torch.equal(_fused(pair, dev, out_dtype=out_dtype), plain)
         for i, act in enumerate(ref.ACTS):
             b = None if i == 1 else bias.to(torch.bfloat16) if i == 2 else bias
             r = None if i == 3 else resw[:, :N] if i == 4 else res
@@ -116,6 +123,20 @@ def test_residual_in_place(pair, M, N, K):
         want = _fused(pair, dev, act=mxg.ACT_SILU, residual=h, out_dtype=dt)
         got = _fused(pair, dev, act=mxg.ACT_SILU, residual=h, out=h, out_dtype=dt)
         assert got is h and torch.equal(got, want)
+
+
+def test_every_kernel_is_reached():
+    """The shapes above take every tile, the decode kernel and a split."""
+    seen, split = set(), 0
+    for pair in PAIRS:
+        for M, N, K in SHAPES:
+            p = mxg.plan_fused(None if pair is None else pair[0], M, N, K,
+                               fmt_b=None if pair is None else pair[1])
+            seen.add((p["tile_m"], p["tile_n"]))
+            split += p["split_k"] > 1
+    log("fused tiles %s, %d split" % (sorted(seen), split))
+    assert seen == {(256, 256), (256, 192), (256, 128), (128, 128), (128, 64), (64, 64), (32, 32)}
+    assert split
 
 
 def test_activation_edges():

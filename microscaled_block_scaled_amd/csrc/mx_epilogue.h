@@ -18,7 +18,7 @@ namespace mx {
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };   // MX_ACT_*
 
 struct Epilogue {
-    static constexpr bool fused = true, stream_b = false;
+    static constexpr bool fused = true, stream_b = false, order_all = true;
     const void *bias;            // N values, null: none
     const void *residual;        // rows of the output's type, pitch ldr, null: none
     int64_t ldr;
@@ -45,18 +45,48 @@ __device__ __forceinline__ float normal_tail(float a)
     return s * t * __builtin_amdgcn_exp2f(a * a * -0.721347520f);      // -log2(e) / 2
 }
 
-__device__ __forceinline__ float act_apply(float v, int act)
+template <int ACT>
+__device__ __forceinline__ float act_of(float v)
 {
-    switch (act) {
-    case ACT_RELU: return v > 0.f ? v : v != v ? v : 0.f;
-    case ACT_SILU: return v * sigmoid(v);
-    case ACT_GELU: {
+    if constexpr (ACT == ACT_RELU) return v > 0.f ? v : v != v ? v : 0.f;
+    if constexpr (ACT == ACT_SILU) return v * sigmoid(v);
+    if constexpr (ACT == ACT_GELU) {
         const float q = normal_tail(fabsf(v));
         return v * (v > 0.f ? 1.f - q : q);
     }
     // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), u = sqrt(2/pi) (v + 0.044715 v^3)
-    case ACT_GELU_TANH: return v * sigmoid(1.59576912f * v * fmaf(0.044715f * v, v, 1.f));
+    if constexpr (ACT == ACT_GELU_TANH)
+        return v * sigmoid(1.59576912f * v * fmaf(0.044715f * v, v, 1.f));
+    return v;
+}
+
+__device__ __forceinline__ float act_apply(float v, int act)
+{
+    switch (act) {
+    case ACT_RELU: return act_of<ACT_RELU>(v);
+    case ACT_SILU: return act_of<ACT_SILU>(v);
+    case ACT_GELU: return act_of<ACT_GELU>(v);
+    case ACT_GELU_TANH: return act_of<ACT_GELU_TANH>(v);
     default: return v;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_16(v4f (&v)[4])
+{
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[u][q] = act_of<ACT>(v[u][q]);
+}
+__device__ __forceinline__ void act_apply16(v4f (&v)[4], int act)
+{
+    switch (act) {
+    case ACT_RELU: act_16<ACT_RELU>(v); break;
+    case ACT_SILU: act_16<ACT_SILU>(v); break;
+    case ACT_GELU: act_16<ACT_GELU>(v); break;
+    case ACT_GELU_TANH: act_16<ACT_GELU_TANH>(v); break;
+    default: break;
     }
 }
 
@@ -86,114 +116,146 @@ __device__ __forceinline__ float epilogue_at(const EP &ep, float v, int64_t m, i
     return act_apply(v + bias_at(ep, n), ep.act) + residual_at<OUT>(ep, m, n);
 }
 
-// U consecutive values of C's type at p (p aligned to them).
-template <int OUT, int U>
-__device__ __forceinline__ void read_c(const void *p, float (&v)[U])
+// U values of C's type as they are in memory: 16, 4 or 2 bytes.
+template <int BYTES> struct c_unit;
+template <> struct c_unit<16> { typedef v4i t; };
+template <> struct c_unit<4> { typedef uint32_t t; };
+template <> struct c_unit<2> { typedef uint16_t t; };
+
+template <int OUT, int U, typename T>
+__device__ __forceinline__ void add_unit(const T &r, float (&v)[U])
 {
-    if constexpr (OUT == OF32) {
-        if constexpr (U == 4) *(v4f *)v = *(const v4f *)p;
-        else v[0] = *(const float *)p;
-    } else if constexpr (U == 1) {
-        v[0] = __uint_as_float((uint32_t)*(const uint16_t *)p << 16);
+    if constexpr (U == 1) {
+        v[0] += __uint_as_float(OUT == OF32 ? (uint32_t)r : (uint32_t)r << 16);
     } else {
-        uint32_t w[U / 2];
-        if constexpr (U == 8) *(v4i *)w = *(const v4i *)p;
-        else w[0] = *(const uint32_t *)p;
+        uint32_t w[sizeof(T) / 4];
+        __builtin_memcpy(w, &r, sizeof(T));
 #pragma unroll
-        for (int i = 0; i < U / 2; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int i = 0; i < U; ++i)
+            v[i] += __uint_as_float(OUT == OF32 ? w[i] : (i & 1) ? w[i / 2] & 0xffff0000u
+                                                                  : w[i / 2] << 16);
     }
 }
-template <int OUT, int U>
-__device__ __forceinline__ void write_c(void *p, const float (&v)[U])
+template <int OUT, int U, typename T>
+__device__ __forceinline__ T make_unit(const float (&v)[U])
 {
+    T r;
     if constexpr (OUT == OF32) {
-        if constexpr (U == 4) *(v4f *)p = *(const v4f *)v;
-        else *(float *)p = v[0];
+        __builtin_memcpy(&r, v, sizeof(T));
     } else if constexpr (U == 1) {
-        *(uint16_t *)p = f32_to_bf16(v[0]);
+        r = f32_to_bf16(v[0]);
     } else {
         uint32_t w[U / 2];
 #pragma unroll
         for (int i = 0; i < U / 2; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
-        if constexpr (U == 8) *(v4i *)p = *(const v4i *)w;
-        else *(uint32_t *)p = w[0];
+        __builtin_memcpy(&r, w, sizeof(T));
     }
+    return r;
 }
 
-// A band's residual and stores, U values at a time: consecutive lanes take
-// consecutive units of a row, eight rounds of the wave's residual loads
-// before their stores, so that their latency is paid once per eight.  (C may
-// be the residual: an element's only reader is the thread that stores it.)
-template <int OUT, int WTN, int PITCH, int U>
-__device__ __forceinline__ void store_band(const Epilogue &ep, const uint8_t *stage, void *C,
-                                           int row0, int col0, int M, int N, int lane)
+// The largest divisor of n that is at most `most`.
+constexpr int part_of(int n, int most)
+{
+    int d = n < most ? n : most;
+    while (n % d) --d;
+    return d;
+}
+
+// The tile kernel's epilogue for a wave's FM bands of 32 rows and WTN
+// columns, U values at a time, consecutive lanes taking consecutive units of
+// a row.  stage_band writes a band's sums (bias added) to the wave's LDS.
+// The residual is read ahead, up to 8 or 16 units a lane: all bands' before
+// the first is staged, or a band's first part before its activation and each
+// further part before its stores, so its latency is met seldom; one load per store and wait for it cost 10 us
+// on 293 x 3443 x 2688.  (C may be the residual: an element's only
+// reader is the thread that stores it.)
+template <int OUT, int WTN, int PITCH, int FM, int U, typename Stage>
+__device__ __forceinline__ void fused_rows(const Epilogue &ep, Stage stage_band, uint8_t *stage,
+                                           void *C, int row0, int col0, int M, int N, int lane)
 {
     typedef typename std::conditional<OUT == OF32, float, uint16_t>::type otype;
-    constexpr int UPR = WTN / U, NIT = (32 * UPR + 63) / 64;    // units per row, rounds
-    constexpr int NB = NIT < 8 ? NIT : 8;
-#pragma unroll 1
-    for (int b = 0; b < NIT; b += NB) {
-        float res[NB][U];
-        if (ep.residual) {
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int t = (b + i) * 64 + lane, row = row0 + t / UPR, col = col0 + t % UPR * U;
-                if (t < 32 * UPR && row < M && col < N)
-                    read_c<OUT, U>((const otype *)ep.residual + row * ep.ldr + col, res[i]);
-            }
-        }
+    typedef typename c_unit<U * sizeof(otype)>::t T;
+    constexpr int UPR = WTN / U, NIT = (32 * UPR + 63) / 64;    // units per row, per lane
+    constexpr int MOST = sizeof(T) == 16 ? 8 : 16;              // units read ahead
+    constexpr bool AHEAD = FM * NIT <= MOST;
+    constexpr int NB = part_of(NIT, MOST);                      // units per part of a band
+    T res[AHEAD ? FM : 1][NB];
+    auto load = [&](int band, int first, T (&r)[NB]) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const int t = (b + i) * 64 + lane, r = t / UPR, c = t % UPR * U;
-            if (t >= 32 * UPR || row0 + r >= M || col0 + c >= N) continue;
-            const float *src = (const float *)(stage + r * PITCH) + c;
-            float v[U];
-            if constexpr (U >= 4) {
-#pragma unroll
-                for (int q = 0; q < U; q += 4) *(v4f *)(v + q) = *(const v4f *)(src + q);
-            } else {
-#pragma unroll
-                for (int q = 0; q < U; ++q) v[q] = src[q];
-            }
-            if (ep.residual) {
-#pragma unroll
-                for (int q = 0; q < U; ++q) v[q] += res[i][q];
-            }
-            write_c<OUT, U>((otype *)C + (int64_t)(row0 + r) * N + col0 + c, v);
+            const int t = (first + i) * 64 + lane;
+            const int row = row0 + band * 32 + t / UPR, col = col0 + t % UPR * U;
+            if (t < 32 * UPR && row < M && col < N)
+                r[i] = *(const T *)((const otype *)ep.residual + row * ep.ldr + col);
         }
+    };
+    if (AHEAD && ep.residual) {
+#pragma unroll
+        for (int b = 0; b < FM; ++b) load(b, 0, res[AHEAD ? b : 0]);
     }
+    static_for<FM>([&](auto bc) {
+        constexpr int b = decltype(bc)::value;
+        stage_band(bc);
+        if (!AHEAD && ep.residual) load(b, 0, res[0]);
+        if (ep.act != ACT_NONE) {
+            // in place, 16 values a lane and turn: enough independent chains
+            // to keep the wave busy, one copy of the code per band
+            constexpr int QPR = WTN / 4;                        // float4 per row
+            static_assert(QPR % 8 == 0, "whole turns");
+#pragma unroll 1
+            for (int t0 = lane; t0 < 32 * QPR; t0 += 256) {
+                v4f v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int t = t0 + u * 64;
+                    v[u] = *(const v4f *)(stage + (t / QPR) * PITCH + (t % QPR) * 16);
+                }
+                act_apply16(v, ep.act);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int t = t0 + u * 64;
+                    *(v4f *)(stage + (t / QPR) * PITCH + (t % QPR) * 16) = v[u];
+                }
+            }
+        }
+#pragma unroll 1
+        for (int first = 0; first < NIT; first += NB) {
+            if (first && ep.residual) load(b, first, res[AHEAD ? b : 0]);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int t = (first + i) * 64 + lane, r = t / UPR, c = t % UPR * U;
+                const int row = row0 + b * 32 + r;
+                if (t >= 32 * UPR || row >= M || col0 + c >= N) continue;
+                const float *src = (const float *)(stage + r * PITCH) + c;
+                float v[U];
+                if constexpr (U >= 4) {
+#pragma unroll
+                    for (int q = 0; q < U; q += 4) *(v4f *)(v + q) = *(const v4f *)(src + q);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < U; ++q) v[q] = src[q];
+                }
+                if (ep.residual) add_unit<OUT, U>(res[AHEAD ? b : 0][i], v);
+                *(T *)((otype *)C + (int64_t)row * N + col0 + c) = make_unit<OUT, U, T>(v);
+            }
+        }
+    });
 }
 
-// The tile kernel's epilogue of one 32-row band of a wave's sub-tile: sums
-// (bias added) in the wave's LDS at `stage`, WTN columns, row pitch PITCH
-// bytes.  First the activation, in place and in a loop that is not unrolled
-// (one copy of its code), then residual and stores in the widest units that
-// divide the rows of C and of the residual: 16 bytes, 4 bytes, or single
-// values.
-template <int OUT, int WTN, int PITCH, typename EP>
-__device__ __forceinline__ void fused_band(const EP &ep, uint8_t *stage, void *C, int row0,
-                                           int col0, int M, int N, int lane)
+// In the widest units that divide the rows of C and of the residual: 16
+// bytes, 4 bytes, or single values.
+template <int OUT, int WTN, int PITCH, int FM, typename EP, typename Stage>
+__device__ __forceinline__ void fused_store(const EP &ep, Stage stage_band, uint8_t *stage,
+                                            void *C, int row0, int col0, int M, int N, int lane)
 {
-    if (ep.act != ACT_NONE) {
-        constexpr int QPR = WTN / 4;                            // float4 per row
-#pragma unroll 1
-        for (int t = lane; t < 32 * QPR; t += 64) {
-            v4f *p = (v4f *)(stage + (t / QPR) * PITCH + (t % QPR) * 16);
-            v4f v = *p;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = act_apply(v[q], ep.act);
-            *p = v;
-        }
-    }
     constexpr int OS = OUT == OF32 ? 4 : 2;
-    const int64_t rows = (ep.residual ? ep.ldr : 0) | N;        // both pitches' low bits
-    if (rows * OS % 16 == 0) store_band<OUT, WTN, PITCH, 16 / OS>(ep, stage, C, row0, col0, M, N, lane);
-    else if (OS == 4 || rows % 2 == 0)
-        store_band<OUT, WTN, PITCH, 4 / OS>(ep, stage, C, row0, col0, M, N, lane);
-    else store_band<OUT, WTN, PITCH, 1>(ep, stage, C, row0, col0, M, N, lane);
+    const int64_t pitch = (ep.residual ? ep.ldr : 0) | N;       // both pitches' low bits
+    if (pitch * OS % 16 == 0)
+        fused_rows<OUT, WTN, PITCH, FM, 16 / OS>(ep, stage_band, stage, C, row0, col0, M, N, lane);
+    else if (OS == 4 || pitch % 2 == 0)
+        fused_rows<OUT, WTN, PITCH, FM, 4 / OS>(ep, stage_band, stage, C, row0, col0, M, N, lane);
+    else
+        fused_rows<OUT, WTN, PITCH, FM, 1>(ep, stage_band, stage, C, row0, col0, M, N, lane);
 }
 
 // splitk_reduce with the epilogue: C[i] from the sum over slices, in slice

@@ -217,11 +217,12 @@ __device__ __forceinline__ int xcd_run(int b, int T)
 // grid), walked in groups of `gm` M-tiles, so the workgroups sharing an
 // XCD's L2 also share A and B panels.
 __device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n, int gm,
-                                        int &tm, int &tn, bool remap = true)
+                                        int &tm, int &tn, bool remap = true,
+                                        bool order_all = false)
 {
     const int ntiles = tiles_m * tiles_n;
     int t = bid;
-    if (remap && (ntiles & 7) == 0) t = xcd_run(bid, ntiles);
+    if (remap && (order_all || (ntiles & 7) == 0)) t = xcd_run(bid, ntiles);
     const int per_group = gm * tiles_n;
     const int grp = t / per_group, first_m = grp * gm;
     const int gsz = min(tiles_m - first_m, gm);
@@ -249,19 +250,21 @@ struct NoGroups {
 // What the sums of a GEMM become.  NoEpilogue writes them as they are (the
 // fused epilogue is struct Epilogue of mx_epilogue.h).  stream_b: the short
 // tiles read B with the nontemporal hint.
+// order_all: workgroups are ordered per XCD also when their number is no
+// multiple of 8.
 struct NoEpilogue {
-    static constexpr bool fused = false, stream_b = true;
+    static constexpr bool fused = false, stream_b = true, order_all = false;
 };
-// NoEpilogue without that hint: the split-K slices of the fused GEMMs.
+// The split-K slices of the fused GEMMs.
 struct PlainSums {
-    static constexpr bool fused = false, stream_b = false;
+    static constexpr bool fused = false, stream_b = false, order_all = true;
 };
 template <typename EP> __device__ float bias_at(const EP &ep, int n);
 template <int OUT, typename EP>
 __device__ float epilogue_at(const EP &ep, float v, int64_t m, int n);
-template <int OUT, int WTN, int PITCH, typename EP>
-__device__ void fused_band(const EP &ep, uint8_t *stage, void *C, int row0, int col0, int M,
-                           int N, int lane);
+template <int OUT, int WTN, int PITCH, int FM, typename EP, typename Stage>
+__device__ void fused_store(const EP &ep, Stage stage_band, uint8_t *stage, void *C, int row0,
+                            int col0, int M, int N, int lane);
 
 // Compile-time loop: f(std::integral_constant<int, I>) for I = 0 .. N-1.
 template <typename F, int... I>
@@ -391,7 +394,7 @@ tile_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
     const int ntiles = tiles_m * tiles_n;
     const int slice = bid / ntiles;
     int tm, tn;
-    tile_of(bid - slice * ntiles, tiles_m, tiles_n, gm, tm, tn, !GT::grouped);
+    tile_of(bid - slice * ntiles, tiles_m, tiles_n, gm, tm, tn, !GT::grouped, EP::order_all);
     const int m0 = tm * BM, n0 = tn * BN;
     const int kb = slice * kchunk, klen = min(kchunk, K - kb);
     // Row stride, slice bytes per row and slice offset of each operand.
@@ -813,6 +816,20 @@ tile_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
 #pragma unroll
         for (int j = 0; j < FN; ++j) bias[j] = bias_at(ep, min(col0 + j * 32 + lr, N - 1));
     }
+    if constexpr (FUSED) {
+        auto stage_band = [&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    *(float *)(stage + (8 * (e / 4) + 4 * g + (e % 4)) * PITCH +
+                               (j * 32 + lr) * 4) = acc[i][j][e] + bias[j];
+        };
+        fused_store<OUT, WTN, PITCH, FM>(ep, stage_band, stage, C, m0 + wm * WTM, col0, M, N,
+                                         lane);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -821,16 +838,11 @@ tile_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
             for (int e = 0; e < 16; ++e) {
                 const int r = 8 * (e / 4) + 4 * g + (e % 4);
                 otype v;
-                if constexpr (FUSED) v = acc[i][j][e] + bias[j];
-                else if constexpr (OUT == OF32) v = acc[i][j][e];
+                if constexpr (OUT == OF32) v = acc[i][j][e];
                 else v = f32_to_bf16(acc[i][j][e]);
                 *(otype *)(stage + r * PITCH + (j * 32 + lr) * OS) = v;
             }
         const int row0 = m0 + wm * WTM + i * 32;
-        if constexpr (FUSED) {
-            fused_band<OUT, WTN, PITCH>(ep, stage, C, row0, col0, M, N, lane);
-            continue;
-        }
         constexpr int NIT = (32 * CPR + 63) / 64;
 #pragma unroll
         for (int it = 0; it < NIT; ++it) {

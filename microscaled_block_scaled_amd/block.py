@@ -7,6 +7,11 @@ computed by the library's HIP kernels, on the current stream or on ``stream``
 (a raw stream handle).  Outputs and workspaces of a call on another stream
 than the current one are allocated for that stream.
 
+A call with plain tensors on the current device and stream is checked and
+launched in one step by the compiled module _native (csrc/binding.cpp), which
+halves its host time; every other call, wrong arguments among them, takes the
+Python code below.
+
     o = mx_rmsnorm_quantize(x, weight, FMT_E4M3, residual=r)   # o.q, o.q_scale, o.h
     dx, dw = mx_rmsnorm_backward(dy, o.h, o.rstd, weight, dh=dh)
     q, q_scale = mx_swiglu_quantize(gate_up, FMT_E4M3)
@@ -38,6 +43,47 @@ MoePlan = namedtuple("MoePlan", "group_rows row_of")
 MoePlan.__doc__ = """Tokens sorted by expert (mx_moe_sort): rows per expert (int64, on the
 device) and each (token, choice) pair's row in expert order (int32, -1 - row
 for a pair without an expert)."""
+
+
+# The library functions that _native calls, in the order it takes them.
+_NATIVE_ORDER = ("mx_rmsnorm_quantize", "mx_rmsnorm_backward_workspace", "mx_rmsnorm_backward",
+                 "mx_swiglu_quantize", "mx_swiglu_backward", "mx_moe_sort_workspace",
+                 "mx_moe_sort", "mx_moe_gather", "mx_moe_combine", "mx_moe_combine_backward",
+                 "mx_gemm_fused", "mx_gemm_bf16_fused")
+_native = None
+
+
+def native():
+    """The compiled module, bound to the loaded library (raises if it has not
+    been built)."""
+    global _native
+    if _native is None:
+        L = _m.lib()                         # loads torch, which _native links to
+        try:
+            from . import _native as module
+        except ImportError as e:
+            raise RuntimeError("_native.so is not built; run microscaled_block_scaled_amd/build.py "
+                               "(or __graft_entry__.build()): %s" % e)
+        module.bind(tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value
+                          for n in _NATIVE_ORDER))
+        _native = module
+    return _native
+
+
+def _fast(name, stream, like, *args):
+    """The operator's outputs from _native, or None where the call is not one
+    it takes.  ``like`` is the tensor whose device the call runs on."""
+    torch = _torch()
+    if stream is not None or not isinstance(like, torch.Tensor):
+        return None
+    device = like.get_device()
+    if device < 0 or device != torch._C._cuda_getDevice():
+        return None
+    r = getattr(_native or native(), name)(*args, device,
+                                           torch._C._cuda_getCurrentRawStream(device))
+    if r.__class__ is int:
+        _m._raise(r)
+    return r
 
 
 def declare(L):
@@ -75,6 +121,7 @@ def _torch():
     if _torch_module is None:
         import torch
         _codes.update({torch.float32: _m.IN_FP32, torch.bfloat16: _m.IN_BF16})
+        _byte_types.update((torch.uint8, torch.float8_e4m3fn, torch.float8_e8m0fnu))
         _torch_module = torch
     return _torch_module
 
@@ -138,6 +185,21 @@ def _rows(t, name, width=None, rows=None, dtype=None, device=None):
     return ld
 
 
+_byte_types = set()     # torch types of packed elements and scales
+
+
+def _bytes(t, name, device):
+    """Shape of a contiguous 2-D tensor of bytes (packed elements, scales)."""
+    if t.__class__ is not _torch().Tensor or not t.is_cuda or t.dtype not in _byte_types:
+        _m._as_u8(t, name)                   # raises, or knows better
+    shape = t.shape
+    if len(shape) != 2 or not t.is_contiguous():
+        raise ValueError("%s must be 2-D and contiguous" % name)
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    return shape
+
+
 def _vector(t, name, n, device, dtypes):
     _tensor(t, name, device)
     if t.shape != (n,) or not t.is_contiguous():
@@ -166,6 +228,11 @@ def mx_rmsnorm_quantize(x, weight, fmt, residual=None, eps=1e-6, need_y=False, n
     ``fmt`` None gives no q.  ``need_y`` also returns y in x's type,
     ``need_rstd`` the float32 rstd that mx_rmsnorm_backward takes.  Returns
     NormOut(q, q_scale, h, y, rstd)."""
+    r = _fast("rmsnorm_quantize", stream, x, x, weight, residual, 0 if fmt is None else fmt, eps,
+              need_y, need_rstd)
+    if r is not None:
+        q, qs, h, y, rstd = r
+        return NormOut(q, qs, x if h is None else h, y, rstd)
     torch = _torch()
     ldx = _rows(x, "x")
     rows, width = x.shape
@@ -201,6 +268,9 @@ def mx_rmsnorm_backward(dy, h, rstd, weight, dh=None, need_dw=True, stream=None)
     through): (dx, dw), dx in h's type for x and the residual alike, dw
     float32 (None without ``need_dw``).  ``dh`` is the gradient that reaches h
     from its other uses."""
+    r = _fast("rmsnorm_backward", stream, h, dy, h, rstd, weight, dh, need_dw)
+    if r is not None:
+        return r
     torch = _torch()
     ldh = _rows(h, "h")
     rows, width = h.shape
@@ -234,6 +304,9 @@ def mx_rmsnorm_backward(dy, h, rstd, weight, dh=None, need_dw=True, stream=None)
 def mx_swiglu_quantize(gate_up, fmt, stream=None):
     """MX(silu(gate) * up) of rows holding gate then up (rows x 2*width):
     (q, q_scale) in mx_gemm's operand layout."""
+    r = _fast("swiglu_quantize", stream, gate_up, gate_up, fmt)
+    if r is not None:
+        return r
     torch = _torch()
     ld = _rows(gate_up, "gate_up")
     rows, two = gate_up.shape
@@ -257,6 +330,9 @@ def mx_swiglu_quantize(gate_up, fmt, stream=None):
 def mx_swiglu_backward(dy, gate_up, stream=None):
     """Gradient of mx_swiglu_quantize with respect to gate_up (the MX rounding
     passes gradients through), in its type."""
+    r = _fast("swiglu_backward", stream, gate_up, dy, gate_up)
+    if r is not None:
+        return r[0]
     torch = _torch()
     ld = _rows(gate_up, "gate_up")
     rows, two = gate_up.shape
@@ -282,6 +358,9 @@ def mx_moe_sort(ids, experts, stream=None):
     experts - 1 is no expert: its pair comes after all others.  Returns
     MoePlan(group_rows, row_of); ``group_rows.tolist()`` is what
     mx_gemm_grouped takes."""
+    r = _fast("moe_sort", stream, ids, ids, experts)
+    if r is not None:
+        return MoePlan(*r)
     torch = _torch()
     _tensor(ids, "ids")
     if ids.dim() != 2 or not ids.is_contiguous():
@@ -318,6 +397,9 @@ def mx_moe_gather(plan, x, x_scale=None, stream=None):
     rows of its pairs, and likewise its rows of x_scale.  Returns
     (xs, xs_scale) of tokens * top rows (xs_scale None without x_scale); rows
     of pairs without an expert, which come last, are zeros."""
+    r = _fast("moe_gather", stream, x, plan.row_of, x, x_scale)
+    if r is not None:
+        return r
     torch = _torch()
     ld = _rows(x, "x")
     dev = x.device
@@ -359,6 +441,9 @@ def mx_moe_combine(plan, y, weights=None, residual=None, stream=None):
     nothing.  ``weights`` (tokens x top, float32) None counts each row once,
     which is the gradient of mx_moe_gather.  y may leave out the rows of pairs
     without an expert."""
+    r = _fast("moe_combine", stream, y, plan.row_of, y, weights, residual)
+    if r is not None:
+        return r[0]
     torch = _torch()
     ldy = _rows(y, "y")
     dev = y.device
@@ -385,6 +470,9 @@ def mx_moe_combine_backward(plan, dout, y, weights, stream=None):
     """Gradient of mx_moe_combine: (dy, dweights).  dy has y's rows, zeros in
     those of pairs without an expert; dweights is (tokens, top) float32.  The
     residual's gradient is dout itself."""
+    r = _fast("moe_combine_backward", stream, y, plan.row_of, dout, y, weights)
+    if r is not None:
+        return r
     torch = _torch()
     ldy = _rows(y, "y")
     dev = y.device
@@ -444,23 +532,24 @@ def mx_gemm_fused(a, a_scale, b, b_scale, fmt, bias=None, act=ACT_NONE, residual
     act an ACT_* code, residual (M, N) in C's type (any row pitch; may be
     ``out`` itself).  Everything is applied to the FP32 sums before C's one
     rounding to ``out_dtype`` (bfloat16 by default)."""
+    code, tdt = _m._out_code(_torch().bfloat16 if out_dtype is None else out_dtype)
+    r = _fast("gemm_fused", stream, a, fmt, fmt if fmt_b is None else fmt_b, a, a_scale, b, b_scale,
+              bias, act, residual, code, out)
+    if r is not None:
+        return r[0] if out is None else out
     torch = _torch()
     fmt_b = fmt if fmt_b is None else fmt_b
     _fmt(fmt), _fmt(fmt_b)
-    code, tdt = _m._out_code(torch.bfloat16 if out_dtype is None else out_dtype)
-    _m._as_u8(a, "a"), _m._as_u8(b, "b")
-    _m._as_u8(a_scale, "a_scale"), _m._as_u8(b_scale, "b_scale")
-    M, N = a.shape[0], b.shape[0]
-    K = _m._k_of(fmt, a.shape[1])
-    if _m._k_of(fmt_b, b.shape[1]) != K:
+    dev = a.device if isinstance(a, torch.Tensor) else None
+    M, row_a = _bytes(a, "a", dev)
+    N, row_b = _bytes(b, "b", dev)
+    K = _m._k_of(fmt, row_a)
+    if _m._k_of(fmt_b, row_b) != K:
         raise ValueError("a and b disagree on K")
-    if tuple(a_scale.shape) != (M, K // 32) or tuple(b_scale.shape) != (N, K // 32):
+    if _bytes(a_scale, "a_scale", dev) != (M, K // 32) or \
+            _bytes(b_scale, "b_scale", dev) != (N, K // 32):
         raise ValueError("scales must be (rows, K/32) = (%d, %d) and (%d, %d)"
                          % (M, K // 32, N, K // 32))
-    dev = a.device
-    for t in (b, a_scale, b_scale):
-        if t.device != dev:
-            raise ValueError("all operands must be on the same device")
     bias_code, ldr = _epilogue(M, N, tdt, dev, bias, residual, out)
     L = _m.lib()
     ctx, s = _enter(dev, stream)
@@ -479,8 +568,11 @@ def mx_gemm_fused(a, a_scale, b, b_scale, fmt, bias=None, act=ACT_NONE, residual
 def mx_gemm_bf16_fused(a, b, bias=None, act=ACT_NONE, residual=None, out_dtype=None, out=None,
                        stream=None):
     """mx_gemm_fused with mx_gemm_bf16's dense BF16 operands."""
+    code, tdt = _m._out_code(_torch().bfloat16 if out_dtype is None else out_dtype)
+    r = _fast("gemm_bf16_fused", stream, a, a, b, bias, act, residual, code, out)
+    if r is not None:
+        return r[0] if out is None else out
     torch = _torch()
-    code, tdt = _m._out_code(torch.bfloat16 if out_dtype is None else out_dtype)
     _m._as_bf16(a, "a"), _m._as_bf16(b, "b")
     M, K = a.shape
     N = b.shape[0]

@@ -1,7 +1,9 @@
-"""Build libmxgemm.so, the gfx950 MX GEMM library, with hipcc (in-tree)."""
+"""Build libmxgemm.so, the gfx950 MX GEMM library, with hipcc, and _native.so,
+the compiled half of block.py, with g++ against torch's headers (in-tree)."""
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -25,6 +27,26 @@ FLAGS = [
 ]
 
 
+NATIVE = os.path.join(HERE, "_native.so")
+NATIVE_SOURCE = os.path.join(CSRC, "binding.cpp")
+
+
+def native_command(out):
+    """The command that builds binding.cpp: host code only, no HIP headers."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    system = [os.path.join(base, "include"),
+              os.path.join(base, "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"]]
+    libs = os.path.join(base, "lib")
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+             "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+             "-I", os.path.join(ROOT, "include")]
+            + [x for d in system for x in ("-isystem", d)]
+            + [NATIVE_SOURCE, "-o", out, "-L" + libs, "-lc10", "-ltorch_cpu", "-ltorch_python",
+               "-Wl,-rpath," + libs])
+
+
 def _run(cmd):
     return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
 
@@ -34,7 +56,7 @@ def _finish(procs, what):
         out, _ = proc.communicate()
         if proc.returncode != 0:
             sys.stderr.write(out)
-            raise RuntimeError("hipcc failed building %s" % what)
+            raise RuntimeError("the compiler failed building %s" % what)
         yield out
 
 
@@ -44,10 +66,13 @@ def build(verbose: bool = False) -> str:
     cmds = [[HIPCC] + [f for f in FLAGS if f != "-shared"] + ["-c", src, "-o", obj]
             for src, obj in zip(SOURCES, objs)]
     link = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC"] + objs + ["-o", tmp]
+    native = native_command(NATIVE + ".tmp")
     if verbose:
-        for cmd in cmds + [link]:
+        for cmd in cmds + [native, link]:
             print(" ".join(cmd), flush=True)
-    outs = list(_finish([_run(c) for c in cmds], "libmxgemm.so"))
+    procs = [_run(c) for c in cmds]
+    outs = list(_finish([_run(native)], "_native.so"))
+    outs += list(_finish(procs, "libmxgemm.so"))
     outs += list(_finish([_run(link)], "libmxgemm.so"))
     for obj in objs:
         os.remove(obj)
@@ -56,6 +81,7 @@ def build(verbose: bool = False) -> str:
         lines = [l for out in outs for l in out.splitlines() if "packed-fp32-ops" not in l]
         if lines:
             print("\n".join(lines))
+    os.replace(NATIVE + ".tmp", NATIVE)
     os.replace(tmp, LIB)
     return LIB
 

@@ -18,6 +18,7 @@ namespace mx {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortBins = kMaxGroups + 1;       // the experts, and no expert
+constexpr int kSortParts = kSortThreads / 256;  // threads that share a bin's counts
 
 struct SortArgs {
     const void *ids;
@@ -91,34 +92,53 @@ __global__ void __launch_bounds__(kSortThreads)
 moe_sort(SortArgs a)
 {
     __shared__ int cnt[kSortWaves][kSortBins + 1];
-    __shared__ int scan[kSortBins];
+    __shared__ int sums[2][kSortParts][kSortBins];           // in all, in earlier chunks
+    __shared__ int wave_total[kSortThreads / 64];
     const int bits = 32 - __clz(a.experts), bins = a.experts + 1;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     sort_count(a, cnt, bits);
-    int before = 0, total = 0;                   // this bin's pairs in earlier chunks, in all
-    if (tid < bins) {
-        if constexpr (MANY) {
+    // Each bin's pairs: kSortParts threads per bin take every kSortParts-th
+    // chunk (or wave), so that few loads follow one another.
+    {
+        const int part = tid / 256;
+        for (int b = tid % 256; b < bins; b += 256) {
+            int total = 0, before = 0;
+            if constexpr (MANY) {
 #pragma unroll 16
-            for (int c = 0; c < (int)gridDim.x; ++c) {
-                const int v = a.counts[(int64_t)c * bins + tid];
-                total += v;
-                before += c < (int)blockIdx.x ? v : 0;
+                for (int c = part; c < (int)gridDim.x; c += kSortParts) {
+                    const int v = a.counts[(int64_t)c * bins + b];
+                    total += v;
+                    before += c < (int)blockIdx.x ? v : 0;
+                }
+            } else {
+                for (int w = part; w < kSortWaves; w += kSortParts) total += cnt[w][b];
             }
-        } else {
-            for (int w = 0; w < kSortWaves; ++w) total += cnt[w][tid];
+            sums[0][part][b] = total;
+            sums[1][part][b] = before;
         }
-        scan[tid] = total;
-        if (blockIdx.x == 0 && tid < a.experts) a.group_rows[tid] = total;
     }
     __syncthreads();
-    for (int d = 1; d < bins; d <<= 1) {         // inclusive sums over the bins
-        const int v = tid >= d && tid < bins ? scan[tid - d] : 0;
-        __syncthreads();
-        if (tid < bins) scan[tid] += v;
-        __syncthreads();
-    }
+    int before = 0, total = 0;
     if (tid < bins) {
-        int at = scan[tid] - total + before;
+#pragma unroll
+        for (int p = 0; p < kSortParts; ++p) {
+            total += sums[0][p][tid];
+            before += sums[1][p][tid];
+        }
+        if (blockIdx.x == 0 && tid < a.experts) a.group_rows[tid] = total;
+    }
+    // first row of each bin: sums over the earlier bins, a wave at a time
+    int upto = total;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 63) wave_total[wave] = upto;
+    __syncthreads();
+    if (tid < bins) {
+        int at = upto - total + before;
+        for (int w = 0; w < wave; ++w) at += wave_total[w];
         for (int w = 0; w < kSortWaves; ++w) {
             const int v = cnt[w][tid];
             cnt[w][tid] = at;

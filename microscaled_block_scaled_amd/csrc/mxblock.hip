@@ -64,6 +64,9 @@ void with_fmt(int dtype, int fmt, Fn f)
     }
 }
 
+#ifndef WIDE_ROWS
+#define WIDE_ROWS (2 * kCUs)
+#endif
 // Calls f(MAXT, C, threads): chunks of 8 values per thread, the threads of a
 // row's workgroup, and the most threads of that kernel.  One chunk per thread
 // (`wide`) has the most loads in flight per row and the shortest row; two
@@ -90,7 +93,10 @@ int64_t norm_grad_groups(int64_t rows) { return std::min<int64_t>(rows, kCUs); }
 
 // Pairs per workgroup of the sort: all of them up to kSortOne, else a 256th
 // part in whole 1024-pair steps of the workgroup, 2048 at least.
-constexpr int64_t kSortOne = 8192;
+#ifndef SORT1
+#define SORT1 8192
+#endif
+constexpr int64_t kSortOne = SORT1;
 int64_t sort_chunk(int64_t n)
 {
     if (n <= kSortOne) return cdiv(n, mx::kSortThreads) * mx::kSortThreads;
@@ -129,7 +135,7 @@ extern "C" int mx_rmsnorm_quantize(int fmt, int dtype, int w_dtype, int64_t rows
     const mx::NormArgs a{X, R, W, H, Y, (uint8_t *)Q, (uint8_t *)Q_scale, rstd, rows, ldx, ldr,
                          (int)width, w_dtype == MX_IN_BF16, eps};
     with_fmt(dtype, Q ? fmt : MX_FMT_E4M3, [&](auto in, auto f) {
-        with_row(rows <= 2 * kCUs, width, [&](auto t, auto c, int threads) {
+        with_row(rows <= WIDE_ROWS, width, [&](auto t, auto c, int threads) {
             hipLaunchKernelGGL((mx::norm_quantize<in(), f(), t(), c()>), dim3(stride_grid(rows)),
                                dim3(threads), 0, (hipStream_t)stream, a);
         });

@@ -118,10 +118,10 @@ bool fused_pair(int fmt_a, int fmt_b)
 // share of the tiles, so the tiles cost ceil(tiles / CUs) * cost per K-value,
 // and splitting K adds a second kernel and a round trip of the planes.  The
 // costs per tile and the two constants were fitted to times of all tiles and
-// splits over 51 shapes (M 20 .. 2048, N 1000 .. 28672, K 1024 .. 28672, each
+// splits over 75 shapes (M 20 .. 2048, N 1000 .. 28672, K 1024 .. 28672, each
 // with bias and residual, operands rotating) in E4M3, E2M1, E4M3 x E2M1 and
 // BF16 on MI355X: the choice takes 1.02 times the best tile and split's time
-// (geometric mean; worst 1.26), the unfused plan's choice 1.55 times (worst
+// (geometric mean; worst 1.28), the unfused plan's choice 1.55 times (worst
 // 3.1).  In E4M3 293 x 3443 x 2688 takes 13 us against 26, 453 x 1628 x 1664
 // 7.8 against 18.6.
 void fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, mx_plan_t *p)

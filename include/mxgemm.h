@@ -470,8 +470,7 @@ int mx_hbm_read_ceiling(const void *src, int64_t bytes, uint32_t *out, void *str
  *   - errors, asynchrony and determinism are as for mx_gemm.  An output
  *     overlaps no input unless it says otherwise.  They allocate nothing and
  *     can be captured in a graph; where a workspace is needed it is the
- *     caller's, used on `stream` until the call's work is done there (the
- *     fused products use the library's own, as mx_gemm does).
+ *     caller's, used on `stream` until the call's work is done there.
  */
 
 /* Longest row of a row operator. */
@@ -609,17 +608,20 @@ enum { MX_ACT_NONE = 0, MX_ACT_RELU = 1, MX_ACT_SILU = 2, MX_ACT_GELU = 3, MX_AC
  *   act        MX_ACT_*
  *   residual   M x N in C's type with pitch ldr, 16-byte aligned, or NULL;
  *              may be C itself (with ldr == N)
- * Everything else as for mx_gemm (with a split K, its per-stream workspace).
+ *   workspace  the plan's workspace_bytes (mx_gemm_fused_plan; often 0),
+ *              16-byte aligned; with less, or NULL, K is not split
+ * Everything else as for mx_gemm.
  */
 int mx_gemm_fused(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, const void *A,
                   const void *A_scale, const void *B, const void *B_scale, const void *bias,
                   int bias_dtype, int act, const void *residual, int64_t ldr, void *C,
-                  int out_dtype, void *stream);
+                  int out_dtype, void *workspace, int64_t workspace_bytes, void *stream);
 
 /* The same on mx_gemm_bf16's operands. */
 int mx_gemm_bf16_fused(int64_t M, int64_t N, int64_t K, const void *A, const void *B,
                        const void *bias, int bias_dtype, int act, const void *residual,
-                       int64_t ldr, void *C, int out_dtype, void *stream);
+                       int64_t ldr, void *C, int out_dtype, void *workspace,
+                       int64_t workspace_bytes, void *stream);
 
 /*
  * The launch they would make: the decode kernel or a tile (128 x 64 and

@@ -49,7 +49,8 @@ for a pair without an expert)."""
 _NATIVE_ORDER = ("mx_rmsnorm_quantize", "mx_rmsnorm_backward_workspace", "mx_rmsnorm_backward",
                  "mx_swiglu_quantize", "mx_swiglu_backward", "mx_moe_sort_workspace",
                  "mx_moe_sort", "mx_moe_gather", "mx_moe_combine", "mx_moe_combine_backward",
-                 "mx_gemm_fused", "mx_gemm_bf16_fused")
+                 "mx_gemm_fused", "mx_gemm_bf16_fused", "mx_gemm_fused_plan",
+                 "mx_gemm_bf16_fused_plan")
 _native = None
 
 
@@ -104,8 +105,9 @@ def declare(L):
             ("mx_moe_combine_backward", ci, [ci, i64, i64, i64, vp, vp, i64, vp, i64, i64, vp, vp,
                                              vp, vp]),
             ("mx_gemm_fused", ci, [ci, ci, i64, i64, i64, vp, vp, vp, vp, vp, ci, ci, vp, i64, vp,
-                                   ci, vp]),
-            ("mx_gemm_bf16_fused", ci, [i64, i64, i64, vp, vp, vp, ci, ci, vp, i64, vp, ci, vp]),
+                                   ci, vp, i64, vp]),
+            ("mx_gemm_bf16_fused", ci, [i64, i64, i64, vp, vp, vp, ci, ci, vp, i64, vp, ci, vp, i64,
+                                        vp]),
             ("mx_gemm_fused_plan", ci, [ci, ci, i64, i64, i64, ci, vp]),
             ("mx_gemm_bf16_fused_plan", ci, [i64, i64, i64, ci, vp])):
         f = getattr(L, name)
@@ -556,10 +558,12 @@ def mx_gemm_fused(a, a_scale, b, b_scale, fmt, bias=None, act=ACT_NONE, residual
     with ctx:
         if out is None:
             out = torch.empty((M, N), dtype=tdt, device=dev)
+        nbytes = plan_fused(fmt, M, N, K, code, fmt_b)["workspace_bytes"]
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         rc = L.mx_gemm_fused(
             fmt, fmt_b, M, N, K, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(),
             b_scale.data_ptr(), _ptr(bias), bias_code, act, _ptr(residual), ldr, out.data_ptr(),
-            code, s)
+            code, _ptr(ws), nbytes, s)
     if rc:
         _m._raise(rc)
     return out
@@ -587,9 +591,10 @@ def mx_gemm_bf16_fused(a, b, bias=None, act=ACT_NONE, residual=None, out_dtype=N
     with ctx:
         if out is None:
             out = torch.empty((M, N), dtype=tdt, device=dev)
-        rc = L.mx_gemm_bf16_fused(M, N, K, a.data_ptr(), b.data_ptr(), _ptr(bias),
-                                           bias_code, act, _ptr(residual), ldr, out.data_ptr(),
-                                           code, s)
+        nbytes = plan_fused(None, M, N, K, code)["workspace_bytes"]
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        rc = L.mx_gemm_bf16_fused(M, N, K, a.data_ptr(), b.data_ptr(), _ptr(bias), bias_code, act,
+                                  _ptr(residual), ldr, out.data_ptr(), code, _ptr(ws), nbytes, s)
     if rc:
         _m._raise(rc)
     return out

@@ -37,6 +37,8 @@ struct Library {
     decltype(&mx_moe_combine_backward) moe_combine_backward;
     decltype(&mx_gemm_fused) gemm_fused;
     decltype(&mx_gemm_bf16_fused) gemm_bf16_fused;
+    decltype(&mx_gemm_fused_plan) gemm_fused_plan;
+    decltype(&mx_gemm_bf16_fused_plan) gemm_bf16_fused_plan;
 } lib;
 constexpr int kFunctions = sizeof(lib) / sizeof(void *);
 
@@ -355,9 +357,14 @@ PyObject *gemm_fused(Call c)
     bytes_of(as, M, K / 32);
     bytes_of(bs, N, K / 32);
     Ep e(c, M, N);
-    const int rc = lib.gemm_fused((int)fa, (int)fb, M, N, K, ptr(a), ptr(as), ptr(b), ptr(bs),
-                                  ptr(e.bias), e.bias_code, (int)e.act, ptr(e.res), e.ldr, ptr(e.out),
-                                  e.out_code, c.stream);
+    mx_plan_t plan;
+    int rc = lib.gemm_fused_plan((int)fa, (int)fb, M, N, K, e.out_code, &plan);
+    if (rc != MX_OK) return PyLong_FromLong(rc);
+    at::Tensor ws;
+    if (plan.workspace_bytes) ws = c.make({plan.workspace_bytes}, at::kByte);
+    rc = lib.gemm_fused((int)fa, (int)fb, M, N, K, ptr(a), ptr(as), ptr(b), ptr(bs), ptr(e.bias),
+                        e.bias_code, (int)e.act, ptr(e.res), e.ldr, ptr(e.out), e.out_code, ptr(ws),
+                        plan.workspace_bytes, c.stream);
     return outputs(rc, e.out);
 }
 
@@ -369,8 +376,13 @@ PyObject *gemm_bf16_fused(Call c)
     dense(a, {M, K}, at::kBFloat16);
     dense(b, {N, K}, at::kBFloat16);
     Ep e(c, M, N);
-    const int rc = lib.gemm_bf16_fused(M, N, K, ptr(a), ptr(b), ptr(e.bias), e.bias_code, (int)e.act,
-                                       ptr(e.res), e.ldr, ptr(e.out), e.out_code, c.stream);
+    mx_plan_t plan;
+    int rc = lib.gemm_bf16_fused_plan(M, N, K, e.out_code, &plan);
+    if (rc != MX_OK) return PyLong_FromLong(rc);
+    at::Tensor ws;
+    if (plan.workspace_bytes) ws = c.make({plan.workspace_bytes}, at::kByte);
+    rc = lib.gemm_bf16_fused(M, N, K, ptr(a), ptr(b), ptr(e.bias), e.bias_code, (int)e.act, ptr(e.res),
+                             e.ldr, ptr(e.out), e.out_code, ptr(ws), plan.workspace_bytes, c.stream);
     return outputs(rc, e.out);
 }
 

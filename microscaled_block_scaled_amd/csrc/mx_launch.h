@@ -112,7 +112,8 @@ bool launch_decode(int fmt_a, int fmt_b, int out_dtype, const void *A, const voi
 // defined in mxfused.hip).  launch_fused returns false if the plan's tile is
 // not compiled.
 bool fused_pair(int fmt_a, int fmt_b);
-void fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, mx_plan_t *p);
+void fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, int max_split,
+                mx_plan_t *p);
 bool launch_fused(int fmt_a, int fmt_b, const mx_plan_t &p, int out_dtype, const void *A,
                   const void *As, const void *B, const void *Bs, void *C, int64_t M, int64_t N,
                   int64_t K, float *W, const mx::Epilogue &ep, hipStream_t s);

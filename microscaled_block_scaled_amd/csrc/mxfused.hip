@@ -124,7 +124,8 @@ bool fused_pair(int fmt_a, int fmt_b)
 // (geometric mean; worst 1.28), the unfused plan's choice 1.55 times (worst
 // 3.1).  In E4M3 293 x 3443 x 2688 takes 13 us against 26, 453 x 1628 x 1664
 // 7.8 against 18.6.
-void fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, mx_plan_t *p)
+void fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, int max_split,
+                mx_plan_t *p)
 {
     // microseconds of a 64 x 64 tile per 128 K-values
     const double unit = fmt_a == kFmtBF16 ? 0.45 : fmt_a == MX_FMT_E2M1 ? 0.16
@@ -133,7 +134,7 @@ void fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, mx_plan_t
     memset(p, 0, sizeof(*p));
     for (const FusedTile &c : kFusedTiles) {
         const int64_t tiles = cdiv(M, c.bm) * cdiv(N, c.bn);
-        for (int req = 1; req <= MX_MAX_SPLIT_K; req *= 2) {
+        for (int req = 1; req <= max_split; req *= 2) {
             const int64_t k = slice_k(K, req);
             const int split = req == 1 ? 1 : (int)cdiv(K, k);
             // slices of at least 1024 K, planes and grid within 32-bit indices

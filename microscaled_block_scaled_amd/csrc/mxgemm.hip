@@ -256,11 +256,12 @@ int device_scratch(int dev, void **ptr)
 
 // Checks that need no device, then the device check, then the launch.  With
 // noalloc the split-K workspace is the device's fixed scratch instead of a
-// stream-ordered allocation; ep, if given, is the fused epilogue.
+// stream-ordered allocation; ep, if given, is the fused epilogue, and its
+// workspace is the caller's.
 int run_plan(const mx_plan_t &plan, int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K,
              const void *A, const void *A_scale, const void *B, const void *B_scale,
              void *C, int out_dtype, void *stream, bool noalloc = false,
-             const mx::Epilogue *ep = nullptr)
+             const mx::Epilogue *ep = nullptr, void *ep_workspace = nullptr)
 {
     const bool scaled = fmt_a != kFmtBF16;
     if (!A || !B || !C || (scaled && (!A_scale || !B_scale))) return MX_ERR_NULL;
@@ -277,7 +278,9 @@ int run_plan(const mx_plan_t &plan, int fmt_a, int fmt_b, int64_t M, int64_t N, 
     float *W = nullptr;
     std::unique_lock<std::mutex> ws_lock(g_ws_mu, std::defer_lock);
     if (plan.workspace_bytes > 0) {
-        if (noalloc) {
+        if (ep) {
+            W = (float *)ep_workspace;
+        } else if (noalloc) {
             void *p = nullptr;
             rc = device_scratch(dev, &p);
             if (rc != MX_OK) return rc;
@@ -478,6 +481,42 @@ int check_epilogue(int64_t N, int out_dtype, const void *bias, int bias_dtype, i
 
 }  // namespace
 
+namespace {
+
+// The plan of a fused GEMM whose arguments are checked: the decode kernel, or
+// the least estimated time with at most max_split slices of K.
+int plan_of_fused(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, int max_split,
+                  mx_plan_t *plan)
+{
+    const bool wide = fmt_b == MX_FMT_E2M1 && fmt_a == MX_FMT_E4M3;
+    if (decode_fits(fmt_a, fmt_b, M, N, K) && decode_preferred(M, N, K, wide))
+        fill_decode_plan(N, plan);
+    else
+        fused_plan(fmt_a, fmt_b, M, N, K, max_split, plan);
+    return plan->workgroups > kMaxGrid ? MX_ERR_SHAPE : MX_OK;
+}
+
+// A fused GEMM whose shape and formats are checked.
+int run_fused(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, const void *A,
+              const void *A_scale, const void *B, const void *B_scale, const void *bias,
+              int bias_dtype, int act, const void *residual, int64_t ldr, void *C, int out_dtype,
+              void *workspace, int64_t workspace_bytes, void *stream)
+{
+    mx_plan_t plan;
+    int rc = plan_of_fused(fmt_a, fmt_b, M, N, K, kMaxSplit, &plan);
+    if (rc == MX_OK && plan.workspace_bytes > (workspace ? workspace_bytes : 0))
+        rc = plan_of_fused(fmt_a, fmt_b, M, N, K, 1, &plan);
+    if (rc != MX_OK) return rc;
+    mx::Epilogue ep;
+    rc = check_epilogue(N, out_dtype, bias, bias_dtype, act, residual, ldr, &ep);
+    if (rc != MX_OK) return rc;
+    if (!aligned(workspace, 16)) return MX_ERR_ALIGN;
+    return run_plan(plan, fmt_a, fmt_b, M, N, K, A, A_scale, B, B_scale, C, out_dtype, stream,
+                    false, &ep, workspace);
+}
+
+}  // namespace
+
 extern "C" int mx_gemm_fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K,
                                   int out_dtype, mx_plan_t *plan)
 {
@@ -485,12 +524,7 @@ extern "C" int mx_gemm_fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, in
     const int rc = check_args(fmt_a, M, N, K, out_dtype);
     if (rc != MX_OK) return rc;
     if (!fused_pair(fmt_a, fmt_b)) return MX_ERR_FORMAT;
-    const bool wide = fmt_b == MX_FMT_E2M1 && fmt_a == MX_FMT_E4M3;
-    if (decode_fits(fmt_a, fmt_b, M, N, K) && decode_preferred(M, N, K, wide))
-        fill_decode_plan(N, plan);
-    else
-        fused_plan(fmt_a, fmt_b, M, N, K, plan);
-    return plan->workgroups > kMaxGrid ? MX_ERR_SHAPE : MX_OK;
+    return plan_of_fused(fmt_a, fmt_b, M, N, K, kMaxSplit, plan);
 }
 
 extern "C" int mx_gemm_bf16_fused_plan(int64_t M, int64_t N, int64_t K, int out_dtype,
@@ -499,39 +533,31 @@ extern "C" int mx_gemm_bf16_fused_plan(int64_t M, int64_t N, int64_t K, int out_
     if (!plan) return MX_ERR_NULL;
     const int rc = check_args_bf16(M, N, K, out_dtype);
     if (rc != MX_OK) return rc;
-    fused_plan(kFmtBF16, kFmtBF16, M, N, K, plan);
-    return plan->workgroups > kMaxGrid ? MX_ERR_SHAPE : MX_OK;
+    return plan_of_fused(kFmtBF16, kFmtBF16, M, N, K, kMaxSplit, plan);
 }
 
 extern "C" int mx_gemm_fused(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K,
                              const void *A, const void *A_scale, const void *B,
                              const void *B_scale, const void *bias, int bias_dtype, int act,
                              const void *residual, int64_t ldr, void *C, int out_dtype,
-                             void *stream)
+                             void *workspace, int64_t workspace_bytes, void *stream)
 {
-    mx_plan_t plan;
-    int rc = mx_gemm_fused_plan(fmt_a, fmt_b, M, N, K, out_dtype, &plan);
+    const int rc = check_args(fmt_a, M, N, K, out_dtype);
     if (rc != MX_OK) return rc;
-    mx::Epilogue ep;
-    rc = check_epilogue(N, out_dtype, bias, bias_dtype, act, residual, ldr, &ep);
-    if (rc != MX_OK) return rc;
-    return run_plan(plan, fmt_a, fmt_b, M, N, K, A, A_scale, B, B_scale, C, out_dtype, stream,
-                    false, &ep);
+    if (!fused_pair(fmt_a, fmt_b)) return MX_ERR_FORMAT;
+    return run_fused(fmt_a, fmt_b, M, N, K, A, A_scale, B, B_scale, bias, bias_dtype, act,
+                     residual, ldr, C, out_dtype, workspace, workspace_bytes, stream);
 }
 
 extern "C" int mx_gemm_bf16_fused(int64_t M, int64_t N, int64_t K, const void *A, const void *B,
                                   const void *bias, int bias_dtype, int act,
                                   const void *residual, int64_t ldr, void *C, int out_dtype,
-                                  void *stream)
+                                  void *workspace, int64_t workspace_bytes, void *stream)
 {
-    mx_plan_t plan;
-    int rc = mx_gemm_bf16_fused_plan(M, N, K, out_dtype, &plan);
+    const int rc = check_args_bf16(M, N, K, out_dtype);
     if (rc != MX_OK) return rc;
-    mx::Epilogue ep;
-    rc = check_epilogue(N, out_dtype, bias, bias_dtype, act, residual, ldr, &ep);
-    if (rc != MX_OK) return rc;
-    return run_plan(plan, kFmtBF16, kFmtBF16, M, N, K, A, nullptr, B, nullptr, C, out_dtype,
-                    stream, false, &ep);
+    return run_fused(kFmtBF16, kFmtBF16, M, N, K, A, nullptr, B, nullptr, bias, bias_dtype, act,
+                     residual, ldr, C, out_dtype, workspace, workspace_bytes, stream);
 }
 
 extern "C" int mx_quantize(int fmt, int in_dtype, int64_t rows, int64_t K,

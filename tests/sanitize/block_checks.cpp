@@ -77,12 +77,13 @@ int main()
                         const int rc = mx_gemm_fused_plan(fa, fb, M, N, K, MX_OUT_BF16, &plan);
                         if (rc == MX_OK) CHECK(plan.workgroups > 0 && plan.workspace_bytes >= 0);
                         const int call = mx_gemm_fused(fa, fb, M, N, K, p, p, p, p, p, MX_IN_FP32,
-                                                       MX_ACT_GELU, p, N, p, MX_OUT_BF16, nullptr);
+                                                       MX_ACT_GELU, p, N, p, MX_OUT_BF16, p, big,
+                                                       nullptr);
                         CHECK(rc == MX_OK ? call == none : call == rc);
                     }
                 const int rc = mx_gemm_bf16_fused_plan(M, N, K, MX_OUT_FP32, &plan);
                 const int call = mx_gemm_bf16_fused(M, N, K, p, p, nullptr, 0, MX_ACT_NONE, nullptr, 0,
-                                                    p, MX_OUT_FP32, nullptr);
+                                                    p, MX_OUT_FP32, nullptr, 0, nullptr);
                 CHECK(rc == MX_OK ? call == none : call == rc);
             }
     for (int code : {MX_ERR_ROW_SHAPE, MX_ERR_WORKSPACE, MX_ERR_ACT}) CHECK(mx_strerror(code)[0] != 'u' || code == MX_ERR_ACT);

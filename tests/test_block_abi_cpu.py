@@ -136,10 +136,11 @@ def test_combine(name, base, over, what):
 
 
 FUSED = dict(fa=2, fb=1, M=8, N=64, K=512, A=G, As=G, B=G, Bs=G, bias=G, bdt=1, act=2, res=G, ldr=64,
-             C=G, out=2, stream=None)
+             C=G, out=2, ws=None, bytes=0, stream=None)
 
 
 @pytest.mark.parametrize("over,code", [
+    (dict(ws=G, bytes=1 << 30), None), (dict(ws=G + 8), mxg.MX_ERR_ALIGN),
     ({}, None), (dict(fa=1, fb=1), None), (dict(fa=2, fb=2), None), (dict(fa=1, fb=2), mxg.MX_ERR_FORMAT),
     (dict(fa=3, fb=3), mxg.MX_ERR_FORMAT), (dict(fa=0), mxg.MX_ERR_FORMAT),
     (dict(fb=6), mxg.MX_ERR_FORMAT), (dict(out=3), mxg.MX_ERR_OUT_DTYPE), (dict(K=192), mxg.MX_ERR_SHAPE),

@@ -139,6 +139,31 @@ def test_every_kernel_is_reached():
     assert split
 
 
+@pytest.mark.parametrize("pair", PAIRS, ids=PAIR_IDS)
+def test_without_a_workspace_k_is_not_split(pair):
+    """The same call through the C ABI with too small a workspace: unsplit, so
+    mx_gemm's unsplit result bit for bit, and nothing written beside C."""
+    torch = _torch()
+    M, N, K = 70, 512, 8192
+    dev, _, _, _ = _case(pair, M, N, K, seed=9)
+    plan = mxg.plan_fused(None if pair is None else pair[0], M, N, K,
+                          fmt_b=None if pair is None else pair[1])
+    assert plan["split_k"] > 1
+    want = _plain(pair, dev, out_dtype=torch.float32, tile=(256, 128), split_k=1)
+    ws = torch.full((plan["workspace_bytes"],), 7, dtype=torch.uint8, device="cuda")
+    for w, nbytes in ((None, 0), (None, 1 << 40), (ws, plan["workspace_bytes"] - 1)):
+        log("fused without workspace %s %s" % (pair, nbytes))
+        out = torch.zeros((M, N), device="cuda")
+        p = [t.data_ptr() for t in dev]
+        tail = [None, 0, mxg.ACT_NONE, None, 0, out.data_ptr(), mxg.OUT_FP32,
+                None if w is None else w.data_ptr(), nbytes,
+                torch.cuda.current_stream().cuda_stream or None]
+        rc = mxg.lib().mx_gemm_bf16_fused(M, N, K, *p, *tail) if pair is None else \
+            mxg.lib().mx_gemm_fused(pair[0], pair[1], M, N, K, *p, *tail)
+        torch.cuda.synchronize()
+        assert rc == mxg.MX_OK and torch.equal(out, want) and (ws == 7).all()
+
+
 def test_activation_edges():
     """Signed zeros, far tails, NaN and infinities through each activation: a
     product of exact values, so the sums are known."""
@@ -193,6 +218,9 @@ def test_graph_replays():
     r = torch.randn((8, 1024), device="cuda").to(torch.bfloat16)
     w = torch.ones(1024, device="cuda")
     qb, sb = mxg.mx_quantize(torch.randn((2048, 1024), device="cuda"), mxg.FMT_E4M3)
+    qk, sk = mxg.mx_quantize(torch.randn((512, 8192), device="cuda"), mxg.FMT_E4M3)
+    long, ls = mxg.mx_quantize(torch.randn((70, 8192), device="cuda"), mxg.FMT_E4M3)
+    assert mxg.plan_fused(mxg.FMT_E4M3, 70, 512, 8192)["split_k"] > 1
     ids = torch.randint(-1, 4, (8, 2), device="cuda")
     wt = torch.rand((8, 2), device="cuda")
 
@@ -203,7 +231,8 @@ def test_graph_replays():
         gu = mxg.mx_gemm_fused(xs, ss, qb, sb, mxg.FMT_E4M3, act=mxg.ACT_NONE)
         q, s = mxg.mx_swiglu_quantize(gu, mxg.FMT_E4M3)
         y = mxg.mx_gemm_fused(q, s, qb[:1024], sb[:1024], mxg.FMT_E4M3)
-        return mxg.mx_moe_combine(plan, y, wt, residual=o.h), q, s, plan.row_of
+        split = mxg.mx_gemm_fused(long, ls, qk, sk, mxg.FMT_E4M3, act=mxg.ACT_GELU)
+        return mxg.mx_moe_combine(plan, y, wt, residual=o.h), q, s, plan.row_of, split
 
     block()
     torch.cuda.synchronize()
@@ -212,6 +241,7 @@ def test_graph_replays():
         out = block()
     for i in range(4):
         x.copy_(torch.randn((8, 1024), device="cuda").to(torch.bfloat16))
+        long.copy_(mxg.mx_quantize(torch.randn((70, 8192), device="cuda"), mxg.FMT_E4M3)[0])
         ids.copy_(torch.randint(-1, 4, (8, 2), device="cuda"))
         want = [t.clone() for t in block()]
         torch.cuda.synchronize()

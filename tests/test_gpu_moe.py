@@ -55,7 +55,7 @@ def _check_sort(ids, experts, dtype="int64"):
 @pytest.mark.parametrize("dtype", ["int32", "int64"])
 @pytest.mark.parametrize("tokens,top,experts", [
     (1, 1, 1), (1, 8, 256), (5, 3, 4), (64, 2, 8), (63, 1, 2), (1000, 8, 255), (1024, 8, 256),
-    (8191, 1, 7), (8193, 1, 7), (4099, 3, 64), (20001, 6, 128), (70000, 8, 256)])
+    (4096, 1, 7), (4097, 1, 7), (8193, 1, 7), (4099, 3, 64), (20001, 6, 128), (70000, 8, 256)])
 def test_sort(tokens, top, experts, dtype):
     log("sort %dx%d over %d experts, %s" % (tokens, top, experts, dtype))
     _check_sort(_ids(tokens, top, experts, tokens + experts), experts, dtype)

@@ -153,6 +153,7 @@ __device__ __forceinline__ T make_unit(const float (&v)[U])
     return r;
 }
 
+constexpr int gcd_of(int a, int b) { return b ? gcd_of(b, a % b) : a; }
 // The largest divisor of n that is at most `most`.
 constexpr int part_of(int n, int most)
 {
@@ -162,31 +163,38 @@ constexpr int part_of(int n, int most)
 }
 
 // The tile kernel's epilogue for a wave's FM bands of 32 rows and WTN
-// columns, U values at a time, consecutive lanes taking consecutive units of
-// a row.  stage_band writes a band's sums (bias added) to the wave's LDS.
+// columns, U values at a time.  stage_band writes a band's sums (bias added)
+// to the wave's LDS.  L lanes take consecutive units of a row, 64 / L rows at
+// once, SEG times across the row, so that a lane's column and its row within
+// a turn do not change from turn to turn (dividing a running index by 96
+// columns cost more than the stores on the 192-column tile).
+//
 // The residual is read ahead, up to 8 or 16 units a lane: all bands' before
 // the first is staged, or a band's first part before its activation and each
-// further part before its stores, so its latency is met seldom; one load per store and wait for it cost 10 us
-// on 293 x 3443 x 2688.  (C may be the residual: an element's only
-// reader is the thread that stores it.)
+// further part before its stores, so its latency is met seldom; one load per
+// store and wait for it cost 10 us on 293 x 3443 x 2688.  (C may be the
+// residual: an element's only reader is the thread that stores it.)
 template <int OUT, int WTN, int PITCH, int FM, int U, typename Stage>
 __device__ __forceinline__ void fused_rows(const Epilogue &ep, Stage stage_band, uint8_t *stage,
                                            void *C, int row0, int col0, int M, int N, int lane)
 {
     typedef typename std::conditional<OUT == OF32, float, uint16_t>::type otype;
     typedef typename c_unit<U * sizeof(otype)>::t T;
-    constexpr int UPR = WTN / U, NIT = (32 * UPR + 63) / 64;    // units per row, per lane
+    constexpr int UPR = WTN / U, NIT = UPR / 2;                 // units per row, per lane and band
+    constexpr int L = gcd_of(UPR, 64), SEG = UPR / L, RPT = 64 / L;   // RPT: rows per turn
     constexpr int MOST = sizeof(T) == 16 ? 8 : 16;              // units read ahead
     constexpr bool AHEAD = FM * NIT <= MOST;
-    constexpr int NB = part_of(NIT, MOST);                      // units per part of a band
+    constexpr int NB = part_of(NIT / SEG, MOST / SEG > 0 ? MOST / SEG : 1) * SEG;
+    static_assert(NIT % SEG == 0 && NIT % NB == 0 && NB % SEG == 0, "whole turns and parts");
+    const int lrow = lane / L, lcol = lane % L * U;
     T res[AHEAD ? FM : 1][NB];
     auto load = [&](int band, int first, T (&r)[NB]) {
+        const int row = row0 + band * 32 + first / SEG * RPT + lrow;
+        const otype *p = (const otype *)ep.residual + row * ep.ldr + col0 + lcol;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const int t = (first + i) * 64 + lane;
-            const int row = row0 + band * 32 + t / UPR, col = col0 + t % UPR * U;
-            if (t < 32 * UPR && row < M && col < N)
-                r[i] = *(const T *)((const otype *)ep.residual + row * ep.ldr + col);
+            const int dr = i / SEG * RPT, dc = i % SEG * L * U;
+            if (row + dr < M && col0 + lcol + dc < N) r[i] = *(const T *)(p + dr * ep.ldr + dc);
         }
     };
     if (AHEAD && ep.residual) {
@@ -221,22 +229,24 @@ __device__ __forceinline__ void fused_rows(const Epilogue &ep, Stage stage_band,
 #pragma unroll 1
         for (int first = 0; first < NIT; first += NB) {
             if (first && ep.residual) load(b, first, res[AHEAD ? b : 0]);
+            const int r0 = first / SEG * RPT + lrow, row = row0 + b * 32 + r0;
+            const float *src = (const float *)(stage + r0 * PITCH) + lcol;
+            otype *dst = (otype *)C + (int64_t)row * N + col0 + lcol;
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                const int t = (first + i) * 64 + lane, r = t / UPR, c = t % UPR * U;
-                const int row = row0 + b * 32 + r;
-                if (t >= 32 * UPR || row >= M || col0 + c >= N) continue;
-                const float *src = (const float *)(stage + r * PITCH) + c;
+                const int dr = i / SEG * RPT, dc = i % SEG * L * U;
+                if (row + dr >= M || col0 + lcol + dc >= N) continue;
+                const float *s = (const float *)((const uint8_t *)src + dr * PITCH) + dc;
                 float v[U];
                 if constexpr (U >= 4) {
 #pragma unroll
-                    for (int q = 0; q < U; q += 4) *(v4f *)(v + q) = *(const v4f *)(src + q);
+                    for (int q = 0; q < U; q += 4) *(v4f *)(v + q) = *(const v4f *)(s + q);
                 } else {
 #pragma unroll
-                    for (int q = 0; q < U; ++q) v[q] = src[q];
+                    for (int q = 0; q < U; ++q) v[q] = s[q];
                 }
                 if (ep.residual) add_unit<OUT, U>(res[AHEAD ? b : 0][i], v);
-                *(T *)((otype *)C + (int64_t)row * N + col0 + c) = make_unit<OUT, U, T>(v);
+                *(T *)(dst + (int64_t)dr * N + dc) = make_unit<OUT, U, T>(v);
             }
         }
     });

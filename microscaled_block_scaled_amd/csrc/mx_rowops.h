@@ -366,6 +366,81 @@ norm_grad(NormGradArgs a)
     }
 }
 
+// The gradient for few rows in one launch: workgroups 0 .. rows - 1 take a
+// row's dx each, the others 32 columns of dw each, straight from dy and h
+// (dw needs no row sum): 8 threads of 4 columns by blockDim / 8 threads down
+// the rows, joined by halves.
+template <int IN>
+__device__ __forceinline__ v4f load4(const void *p, int64_t at)
+{
+    if constexpr (IN == IN_F32) return *(const v4f *)((const float *)p + at);
+    const uint2 r = *(const uint2 *)((const uint16_t *)p + at);
+    return v4f{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u),
+               __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u)};
+}
+
+template <int IN, int MAXT, int C>
+__global__ void __launch_bounds__(MAXT)
+norm_grad_few(NormGradArgs a, float *dw)
+{
+    __shared__ float part[MAXT / 64];
+    __shared__ v4f sums[MAXT / 8][8];
+    const int tid = threadIdx.x, T = blockDim.x;
+    if (blockIdx.x >= a.rows) {
+        const int cx = tid & 7, ry = tid >> 3, n = T >> 3;
+        const int col = ((int)(blockIdx.x - a.rows) * 8 + cx) * 4;
+        v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int r = ry; r < (int)a.rows; r += n) {
+            const v4f g = load4<IN>(a.dy, r * a.lddy + col), h = load4<IN>(a.h, r * a.ldh + col);
+            const float rstd = a.rstd[r];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = fmaf(g[i], h[i] * rstd, acc[i]);
+        }
+        sums[ry][cx] = acc;
+        __syncthreads();
+        for (int m = n; m > 1;) {
+            const int half = (m + 1) >> 1;
+            if (ry + half < m) sums[ry][cx] += sums[ry + half][cx];
+            __syncthreads();
+            m = half;
+        }
+        if (ry == 0) *(v4f *)(dw + col) = sums[0][cx];
+        return;
+    }
+    const int64_t row = blockIdx.x;
+    const float rstd = a.rstd[row];
+    float gw[C][8], xhat[C][8], dot = 0.f;
+    raw8<IN> dv[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = (c * T + tid) * 8;
+        if (col >= a.width) continue;
+        float w[8];
+        unpack8<IN>(load8<IN>(a.dy, row * a.lddy + col), gw[c]);
+        unpack8<IN>(load8<IN>(a.h, row * a.ldh + col), xhat[c]);
+        unpack_weight(load_weight(a.w, col, a.w_bf16), a.w_bf16, w);
+        if (a.dh) dv[c] = load8<IN>(a.dh, row * a.lddh + col);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            gw[c][i] *= w[i];
+            xhat[c][i] *= rstd;
+            dot = fmaf(gw[c][i], xhat[c][i], dot);
+        }
+    }
+    const float mean = block_sum(dot, part) / (float)a.width;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = (c * T + tid) * 8;
+        if (col >= a.width) continue;
+        float d[8] = {};
+        if (a.dh) unpack8<IN>(dv[c], d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = fmaf(fmaf(-xhat[c][i], mean, gw[c][i]), rstd, d[i]);
+        store8<IN>(a.dx, row * a.width + col, pack8<IN>(d));
+    }
+}
+
 // dw[j] = sum over the n partial rows of part[.][j], in a fixed order: 32
 // columns per workgroup, 32 threads down the rows by 8 threads of 4 columns.
 __global__ void __launch_bounds__(256)

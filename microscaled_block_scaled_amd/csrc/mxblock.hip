@@ -86,6 +86,13 @@ void with_row(int64_t width, Fn f)
 // 8192 x 4096 BF16 53.7 us against 50.5, four 59.0.)
 int64_t norm_grad_groups(int64_t rows) { return std::min<int64_t>(rows, kCUs); }
 
+// Up to this many rows of at most 8192 values the gradient with dw is one
+// launch without partial sums (norm_grad_few), which reads dy and h twice.
+// (A call on 64 x 4096 BF16 7.6 us, with partial sums 11.0; 256 x 8192 7.7 and
+// 12.6; 512 x 4096 8.0 and 10.4; 1024 x 4096 14.1 and 12.9.)
+constexpr int64_t kGradFew = 512;
+bool grad_few(int64_t rows, int64_t width) { return rows > 0 && rows <= kGradFew && width <= 8192; }
+
 // Pairs per workgroup of the sort: all of them up to kSortOne, else a 256th
 // part in whole 1024-pair steps of the workgroup, 2048 at least.  (One
 // workgroup and launch: 1024 pairs 6.3 us a call, two launches 9.6; 4096
@@ -142,7 +149,7 @@ extern "C" int mx_rmsnorm_quantize(int fmt, int dtype, int w_dtype, int64_t rows
 extern "C" int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t width)
 {
     if (!row_shape(rows, width)) return MX_ERR_ROW_SHAPE;
-    return norm_grad_groups(rows) * width * 4;
+    return grad_few(rows, width) ? 0 : norm_grad_groups(rows) * width * 4;
 }
 
 extern "C" int mx_rmsnorm_backward(int dtype, int w_dtype, int64_t rows, int64_t width,
@@ -156,9 +163,9 @@ extern "C" int mx_rmsnorm_backward(int dtype, int w_dtype, int64_t rows, int64_t
         (dH && !pitch_shape(lddh, width)))
         return MX_ERR_ROW_SHAPE;
     if (rows == 0 && !dW) return MX_OK;
-    if ((rows && (!dY || !H || !rstd || !W || !dX)) || (rows && dW && !workspace))
-        return MX_ERR_NULL;
-    if (dW && workspace_bytes < norm_grad_groups(rows) * width * 4) return MX_ERR_WORKSPACE;
+    const int64_t need = dW ? mx_rmsnorm_backward_workspace(rows, width) : 0;
+    if ((rows && (!dY || !H || !rstd || !W || !dX)) || (need && !workspace)) return MX_ERR_NULL;
+    if (workspace_bytes < need) return MX_ERR_WORKSPACE;
     const int64_t es = size_of(dtype);
     if (!aligned(dY, 16) || !aligned(H, 16) || !aligned(W, 16) || !aligned(dH, 16) ||
         !aligned(dX, 16) || !aligned(dW, 16) || !aligned(workspace, 16) || !aligned(rstd, 4) ||
@@ -172,6 +179,20 @@ extern "C" int mx_rmsnorm_backward(int dtype, int w_dtype, int64_t rows, int64_t
     const int64_t groups = norm_grad_groups(rows);
     const mx::NormGradArgs a{dY, H, W, dH, rstd, dX, dW ? (float *)workspace : nullptr, rows,
                              lddy, ldh, lddh, (int)width, w_dtype == MX_IN_BF16};
+    if (dW && grad_few(rows, width)) {
+        with_row<1>(width, [&](auto t, auto c, int threads) {
+            const dim3 grid((unsigned)(rows + width / 32));
+            if constexpr (c() <= 1) {
+                if (dtype == MX_IN_FP32)
+                    hipLaunchKernelGGL((mx::norm_grad_few<mx::IN_F32, t(), c()>), grid,
+                                       dim3(threads), 0, s, a, dW);
+                else
+                    hipLaunchKernelGGL((mx::norm_grad_few<mx::IN_BF16, t(), c()>), grid,
+                                       dim3(threads), 0, s, a, dW);
+            }
+        });
+        return launched();
+    }
     if (groups)
         // one chunk per thread, and with it the next row's loads in flight:
         // 8192 x 4096 BF16 50 us, with two 52

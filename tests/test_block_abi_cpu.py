@@ -61,8 +61,9 @@ NORM_B = dict(dtype=2, w_dtype=1, rows=4, width=64, dY=G, lddy=64, H=G, ldh=64, 
 @pytest.mark.parametrize("over,what", [
     ({}, "dev"), (dict(dtype=7), "dt"), (dict(w_dtype=0), "dt"), (dict(width=33), "shape"),
     (dict(lddy=10), "shape"), (dict(ldh=10), "shape"), (dict(lddh=10), "shape"),
-    (dict(dH=None, lddh=0), "dev"), (dict(bytes=4 * 64 * 4 - 1), "ws"), (dict(bytes=4 * 64 * 4), "dev"),
-    (dict(ws=None), "null"), (dict(ws=None, dW=None, bytes=0), "dev"), (dict(rstd=None), "null"),
+    (dict(dH=None, lddh=0), "dev"), (dict(rows=9000, bytes=256 * 64 * 4 - 1), "ws"),
+    (dict(rows=9000, bytes=256 * 64 * 4), "dev"), (dict(rows=9000, ws=None), "null"),
+    (dict(ws=None, bytes=0), "dev"), (dict(rows=9000, ws=None, dW=None, bytes=0), "dev"), (dict(rstd=None), "null"),
     (dict(dX=None), "null"), (dict(rows=0, dW=None, dY=None), "ok"),
     (dict(rows=0, dY=None, H=None, rstd=None, W=None, dX=None, ws=None, bytes=0), "dev"),
     (dict(dY=G + 2), "align"), (dict(ws=G + 4), "align"), (dict(lddy=65), "align")])
@@ -191,7 +192,9 @@ def test_fused_plans():
 def test_workspaces():
     L = mxg.lib()
     assert L.mx_rmsnorm_backward_workspace(0, 64) == 0
-    assert L.mx_rmsnorm_backward_workspace(3, 64) == 3 * 64 * 4
+    assert L.mx_rmsnorm_backward_workspace(3, 64) == 0
+    assert L.mx_rmsnorm_backward_workspace(3, 8224) == 3 * 8224 * 4
+    assert L.mx_rmsnorm_backward_workspace(9000, 64) == 256 * 64 * 4
     big = L.mx_rmsnorm_backward_workspace(1 << 30, 65536)
     assert 0 < big <= 1024 * 65536 * 4
     assert L.mx_rmsnorm_backward_workspace(3, 65) == mxg.MX_ERR_ROW_SHAPE

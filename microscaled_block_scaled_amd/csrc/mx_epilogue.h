@@ -194,6 +194,7 @@ __device__ __forceinline__ void fused_rows(const Epilogue &ep, Stage stage_band,
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const int dr = i / SEG * RPT, dc = i % SEG * L * U;
+            r[i] = T{};
             if (row + dr < M && col0 + lcol + dc < N) r[i] = *(const T *)(p + dr * ep.ldr + dc);
         }
     };
@@ -232,10 +233,12 @@ __device__ __forceinline__ void fused_rows(const Epilogue &ep, Stage stage_band,
             const int r0 = first / SEG * RPT + lrow, row = row0 + b * 32 + r0;
             const float *src = (const float *)(stage + r0 * PITCH) + lcol;
             otype *dst = (otype *)C + (int64_t)row * N + col0 + lcol;
+            // all values first, then all stores: a wait between a store and the
+            // next value would be for the store itself
+            T(&out)[NB] = res[AHEAD ? b : 0];
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 const int dr = i / SEG * RPT, dc = i % SEG * L * U;
-                if (row + dr >= M || col0 + lcol + dc >= N) continue;
                 const float *s = (const float *)((const uint8_t *)src + dr * PITCH) + dc;
                 float v[U];
                 if constexpr (U >= 4) {
@@ -245,8 +248,13 @@ __device__ __forceinline__ void fused_rows(const Epilogue &ep, Stage stage_band,
 #pragma unroll
                     for (int q = 0; q < U; ++q) v[q] = s[q];
                 }
-                if (ep.residual) add_unit<OUT, U>(res[AHEAD ? b : 0][i], v);
-                *(T *)(dst + (int64_t)dr * N + dc) = make_unit<OUT, U, T>(v);
+                if (ep.residual) add_unit<OUT, U>(out[i], v);
+                out[i] = make_unit<OUT, U, T>(v);
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int dr = i / SEG * RPT, dc = i % SEG * L * U;
+                if (row + dr < M && col0 + lcol + dc < N) *(T *)(dst + (int64_t)dr * N + dc) = out[i];
             }
         }
     });
@@ -269,19 +277,33 @@ __device__ __forceinline__ void fused_store(const EP &ep, Stage stage_band, uint
 }
 
 // splitk_reduce with the epilogue: C[i] from the sum over slices, in slice
-// order, of W[s * plane + i]; n_cols is C's row length.  mn < 2^31.
+// order, of W[s * plane + i]; n_cols is C's row length, mn < 2^30.  A thread
+// takes 4 consecutive values; where all rows (C's and the residual's) are
+// multiples of 4 values they lie in one row and are read and stored together.
 template <int OUT>
 __global__ void __launch_bounds__(256)
 splitk_fused(const float *__restrict__ W, void *C, int mn, int n_cols, int64_t plane, int slices,
              Epilogue ep)
 {
+    typedef typename std::conditional<OUT == OF32, v4f, uint2>::type T;
+    typedef typename std::conditional<OUT == OF32, float, uint16_t>::type otype;
     const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= mn) return;
+    int m = (int)((uint32_t)i / (uint32_t)n_cols), c = i - m * n_cols;
+    const bool whole = (((ep.residual ? ep.ldr : 0) | n_cols) & 3) == 0;
+    T r{};
+    if (whole && ep.residual) r = *(const T *)((const otype *)ep.residual + m * ep.ldr + c);
     v4f acc = *(const v4f *)(W + i);
     for (int s = 1; s < slices; ++s) acc += *(const v4f *)(W + s * plane + i);
-    const int n = min(4, mn - i);
-    int m = (int)((uint32_t)i / (uint32_t)n_cols), c = i - m * n_cols;
-    for (int q = 0; q < n; ++q) {
+    if (whole) {
+        float v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = act_apply(acc[q] + bias_at(ep, c + q), ep.act);
+        if (ep.residual) add_unit<OUT, 4>(r, v);
+        *(T *)((otype *)C + i) = make_unit<OUT, 4, T>(v);
+        return;
+    }
+    for (int q = 0; q < min(4, mn - i); ++q) {
         const float v = epilogue_at<OUT>(ep, acc[q], m, c);
         if (OUT == OF32) ((float *)C)[i + q] = v;
         else ((uint16_t *)C)[i + q] = f32_to_bf16(v);

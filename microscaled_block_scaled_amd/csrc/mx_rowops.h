@@ -442,21 +442,25 @@ norm_grad_few(NormGradArgs a, float *dw)
 }
 
 // dw[j] = sum over the n partial rows of part[.][j], in a fixed order: 32
-// columns per workgroup, 32 threads down the rows by 8 threads of 4 columns.
-__global__ void __launch_bounds__(256)
+// columns per workgroup, 8 threads of 4 columns by 128 threads down the rows,
+// joined by halves.
+__global__ void __launch_bounds__(1024)
 column_sum(const float *__restrict__ part, float *__restrict__ dw, int n, int width)
 {
-    __shared__ v4f sums[32][8];
+    __shared__ v4f sums[128][8];
     const int cx = threadIdx.x & 7, ry = threadIdx.x >> 3;
     const int col = blockIdx.x * 32 + cx * 4;
     v4f acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int r = ry; r < n; r += 32) acc += *(const v4f *)(part + (int64_t)r * width + col);
+#pragma unroll 2
+    for (int r = ry; r < n; r += 128) acc += *(const v4f *)(part + (int64_t)r * width + col);
     sums[ry][cx] = acc;
     __syncthreads();
-    if (ry) return;
-    for (int r = 1; r < 32; ++r) acc += sums[r][cx];
-    *(v4f *)(dw + col) = acc;
+#pragma unroll
+    for (int half = 64; half; half >>= 1) {
+        if (ry < half) sums[ry][cx] += sums[ry + half][cx];
+        __syncthreads();
+    }
+    if (ry == 0) *(v4f *)(dw + col) = sums[0][cx];
 }
 
 // y = silu(gate) * up -> MX, gate and up the two halves of a row of 2 * width

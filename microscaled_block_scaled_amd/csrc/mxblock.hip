@@ -205,7 +205,7 @@ extern "C" int mx_rmsnorm_backward(int dtype, int w_dtype, int64_t rows, int64_t
                                    dim3(threads), 0, s, a);
         });
     if (dW)
-        hipLaunchKernelGGL(mx::column_sum, dim3((unsigned)(width / 32)), dim3(256), 0, s,
+        hipLaunchKernelGGL(mx::column_sum, dim3((unsigned)(width / 32)), dim3(1024), 0, s,
                            (const float *)workspace, dW, (int)groups, (int)width);
     return launched();
 }

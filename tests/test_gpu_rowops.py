@@ -8,7 +8,7 @@ Tolerances, in units u = 2^-24 of FP32 rounding:
   rstd, plus mean, eps, square root and quotient (4 u) and two products: 50 u.
 * norm gradient: 90 u of the row sum's terms, plus the outer arithmetic: 100 u
   of the sum of the terms' magnitudes; dw adds its rows one by one per
-  workgroup (rows / 256), then by 32 threads over 256 partial rows; for few
+  workgroup (rows / 256), then by 128 threads over 256 partial rows; for few
   rows one thread in eight of the row's workgroup walks them.
 * sigmoid: exp2 and reciprocal of 2 u each, their arguments 2 u, the sum and
   the products 1 u each: 10 u; the gradient's products 16 u of the magnitudes.

@@ -491,8 +491,10 @@ int mx_hbm_read_ceiling(const void *src, int64_t bytes, uint32_t *out, void *str
  *              not both be NULL
  *   rstd       rows floats for mx_rmsnorm_backward, or NULL
  *   eps        at least 0
- * A row with a NaN or an infinity gives NaNs in Y and blocks of scale 255
- * with zero codes, as mx_quantize does for such blocks.
+ * A NaN in a row gives NaNs in its Y and blocks of scale 255 with zero codes,
+ * as mx_quantize does for such blocks.  The sum of squares is FP32: a row
+ * with an infinity, or whose squares pass FP32's range, has rstd 0 (its
+ * infinities become NaNs, the rest zeros).
  */
 int mx_rmsnorm_quantize(int fmt, int dtype, int w_dtype, int64_t rows, int64_t width,
                         const void *X, int64_t ldx, const void *R, int64_t ldr, const void *W,

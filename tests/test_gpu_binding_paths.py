@@ -29,3 +29,17 @@ def test_what_is_no_format_is_refused(fmt, path):
         mxg.mx_gemm_fused(q, qs, q, qs, fmt, stream=s)
     with pytest.raises(ValueError):
         mxg.mx_gemm_fused(q, qs, q, qs, mxg.FMT_E4M3, fmt_b=fmt, stream=s)
+
+
+@pytest.mark.parametrize("path", ["compiled", "python"])
+@pytest.mark.parametrize("act", [-1, 5, 1 << 32, (1 << 32) + 1, -(1 << 32)])
+def test_what_is_no_activation_is_refused(act, path):
+    import torch
+    log("activation %d, %s path" % (act, path))
+    s = None if path == "compiled" else _here()
+    q, qs = mxg.mx_quantize(torch.ones((4, 128), device="cuda"), mxg.FMT_E4M3)
+    a = torch.ones((4, 128), device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        mxg.mx_gemm_fused(q, qs, q, qs, mxg.FMT_E4M3, act=act, stream=s)
+    with pytest.raises(ValueError):
+        mxg.mx_gemm_bf16_fused(a, a, act=act, stream=s)

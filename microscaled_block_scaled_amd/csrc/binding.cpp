@@ -76,7 +76,15 @@ struct Call {
         ++at;
         return true;
     }
-    bool flag() { return PyObject_IsTrue(args[at++]) == 1; }
+    bool flag()
+    {
+        const int v = PyObject_IsTrue(args[at++]);
+        if (v < 0) {
+            PyErr_Clear();
+            throw Other{};
+        }
+        return v == 1;
+    }
     double real()
     {
         const double v = PyFloat_AsDouble(args[at++]);

@@ -43,3 +43,21 @@ def test_what_is_no_activation_is_refused(act, path):
         mxg.mx_gemm_fused(q, qs, q, qs, mxg.FMT_E4M3, act=act, stream=s)
     with pytest.raises(ValueError):
         mxg.mx_gemm_bf16_fused(a, a, act=act, stream=s)
+
+
+class _NoTruth:
+    def __bool__(self):
+        raise LookupError("neither true nor false")
+
+
+@pytest.mark.parametrize("path", ["compiled", "python"])
+def test_a_flag_without_truth_raises_its_own_error(path):
+    import torch
+    log("flags without truth, %s path" % path)
+    s = None if path == "compiled" else _here()
+    x, w = torch.ones((4, 64), device="cuda"), torch.ones(64, device="cuda")
+    for kw in (dict(need_y=_NoTruth()), dict(need_y=True, need_rstd=_NoTruth())):
+        with pytest.raises(LookupError):
+            mxg.mx_rmsnorm_quantize(x, w, mxg.FMT_E4M3, stream=s, **kw)
+    with pytest.raises(LookupError):
+        mxg.mx_rmsnorm_backward(x, x, torch.ones(4, device="cuda"), w, need_dw=_NoTruth(), stream=s)

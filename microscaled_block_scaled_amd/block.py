@@ -139,8 +139,11 @@ def _enter(device, stream):
     index = device.index
     current = torch._C._cuda_getCurrentRawStream(index)
     if stream is not None and int(stream) != current:
-        ext = torch.cuda.ExternalStream(int(stream), device)
-        return torch.cuda.stream(ext), int(stream) or None
+        # handle 0 is the default stream; an external stream of 0 would be
+        # some new stream, to which the allocations would belong
+        on = torch.cuda.ExternalStream(int(stream), device) if int(stream) else \
+            torch.cuda.default_stream(device)
+        return torch.cuda.stream(on), int(stream) or None
     if torch._C._cuda_getDevice() != index:
         return torch.cuda.device(device), current or None
     return _HERE, current or None

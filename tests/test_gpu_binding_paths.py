@@ -1,5 +1,6 @@
 """The two ways into the operators between the products -- the compiled one on
-the current stream, the Python one on a named stream -- refuse the same calls."""
+the current stream, the Python one on a named stream -- refuse the same calls,
+and a named stream is the one that a call's allocations belong to."""
 import pytest
 
 import microscaled_block_scaled_amd as mxg
@@ -61,3 +62,29 @@ def test_a_flag_without_truth_raises_its_own_error(path):
             mxg.mx_rmsnorm_quantize(x, w, mxg.FMT_E4M3, stream=s, **kw)
     with pytest.raises(LookupError):
         mxg.mx_rmsnorm_backward(x, x, torch.ones(4, device="cuda"), w, need_dw=_NoTruth(), stream=s)
+
+
+def test_the_default_stream_by_its_handle(monkeypatch):
+    """stream=0 from inside another stream: outputs are allocated for the
+    default stream, on which the call runs, and not for some third one."""
+    import torch
+    log("the default stream by its handle")
+    x, w = torch.randn((4, 64), device="cuda"), torch.ones(64, device="cuda")
+    want = mxg.mx_rmsnorm_quantize(x, w, mxg.FMT_E4M3)
+    torch.cuda.synchronize()
+    entered = []
+    enter = torch.cuda.stream
+
+    def spy(s):
+        entered.append(s.cuda_stream)
+        return enter(s)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        monkeypatch.setattr(torch.cuda, "stream", spy)
+        got = mxg.mx_rmsnorm_quantize(x, w, mxg.FMT_E4M3, stream=0)
+        monkeypatch.undo()
+        assert torch.cuda.current_stream() == side
+    torch.cuda.synchronize()
+    assert entered == [0]
+    assert torch.equal(got.q, want.q) and torch.equal(got.q_scale, want.q_scale)

@@ -96,6 +96,29 @@ __device__ __forceinline__ void saturate_fp8(bool on)
     else __builtin_amdgcn_s_setreg(1 | (23 << 6), 0);
 }
 
+// To the compiler a conversion is pure: nothing in it says that it depends on
+// MODE, so nothing keeps it on its side of saturate_fp8.  Its operands and its
+// result pass through empty volatile asm, which costs no instruction and
+// stays in order with the register writes: what is computed from a held value
+// comes after, what is held was computed before.
+__device__ __forceinline__ void hold(float (&v)[8])
+{
+    asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]),
+                      "+v"(v[6]), "+v"(v[7]));
+}
+
+// pack8 in a kernel that also converts to format F: outside of the windows
+// that 8-bit formats have.
+template <int IN, int F>
+__device__ __forceinline__ raw8<IN> pack8_beside(float (&v)[8])
+{
+    constexpr bool HELD = IN == IN_BF16 && (F == FP8 || F == BF8);
+    if constexpr (HELD) hold(v);
+    raw8<IN> r = pack8<IN>(v);
+    if constexpr (HELD) asm volatile("" : "+v"(r.q[0]));
+    return r;
+}
+
 // MX elements and scale byte of 8 values of a block whose other values are
 // in the other lanes of the lane's group of four, by the conversion rule of
 // quantize_kernel: the same bytes for the same FP32 values.  q addresses the
@@ -141,17 +164,22 @@ __device__ __forceinline__ void quantize8(const float (&v)[8], uint8_t *q, uint8
     } else {
         typedef short s16x2 __attribute__((vector_size(4)));
         s16x2 w[2] = {};
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = v[i];
         saturate_fp8(true);
+        hold(u);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if constexpr (F == BF8) {
-                w[i] = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w[i], v[4 * i], v[4 * i + 1], scale, false);
-                w[i] = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w[i], v[4 * i + 2], v[4 * i + 3], scale, true);
+                w[i] = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w[i], u[4 * i], u[4 * i + 1], scale, false);
+                w[i] = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w[i], u[4 * i + 2], u[4 * i + 3], scale, true);
             } else {
-                w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w[i], v[4 * i], v[4 * i + 1], scale, false);
-                w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w[i], v[4 * i + 2], v[4 * i + 3], scale, true);
+                w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w[i], u[4 * i], u[4 * i + 1], scale, false);
+                w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w[i], u[4 * i + 2], u[4 * i + 3], scale, true);
             }
         }
+        asm volatile("" : "+v"(w[0]), "+v"(w[1]));
         saturate_fp8(false);
         const uint64_t both = (uint64_t)__builtin_bit_cast(uint32_t, w[0]) |
                               ((uint64_t)__builtin_bit_cast(uint32_t, w[1]) << 32);
@@ -247,7 +275,7 @@ norm_quantize(NormArgs a)
                 unpack8<IN>(rv[c], r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[i] += r[i];
-                hv[c] = pack8<IN>(h);
+                hv[c] = pack8_beside<IN, F>(h);
                 store8<IN>(a.h, row * a.width + col, hv[c]);
             }
             unpack8<IN>(hv[c], h);
@@ -267,7 +295,7 @@ norm_quantize(NormArgs a)
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = h[i] * rstd * w[i];
             const int64_t at = row * a.width + col;
-            if (a.y) store8<IN>(a.y, at, pack8<IN>(y));
+            if (a.y) store8<IN>(a.y, at, pack8_beside<IN, F>(y));
             if (a.q) quantize8<F>(y, a.q + at / 8 * mx8<F>::bytes, a.s + at / 32, (tid & 3) == 0);
         }
     }

@@ -1,0 +1,130 @@
+"""What the compiler is held to in the kernels between the products (CPU only:
+their gfx950 code is compiled here and read, not run).
+
+Conversions to 8-bit floats saturate while a bit of the MODE register is set,
+and BF16 conversions must not run while it is.  Both are pure to the compiler,
+so the source ties them to the register writes by empty volatile asm; that it
+does is read from the intermediate code, and that the instructions come out in
+that order from the assembly."""
+import os
+import re
+import subprocess
+
+import pytest
+
+from microscaled_block_scaled_amd import build as B
+
+CVT8 = ("llvm.amdgcn.cvt.scalef32.pk.fp8.f32", "llvm.amdgcn.cvt.scalef32.pk.bf8.f32")
+
+
+def compiled(source, out, *more):
+    """Text of a source's gfx950 code: intermediate code or assembly."""
+    if not os.path.exists(B.HIPCC):
+        pytest.skip("no hipcc")
+    cmd = [B.HIPCC] + [f for f in B.FLAGS if f != "-shared"] + ["--cuda-device-only", "-S"]
+    r = subprocess.run(cmd + list(more) + [source, "-o", out], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    return open(out).read()
+
+
+def functions(ir):
+    """{name: lines} of the kernels of intermediate code."""
+    found = {}
+    for m in re.finditer(r"^define [^\n]*@(\S+?)\([^\n]*\{\n(.*?)^\}", ir, re.M | re.S):
+        found[m.group(1)] = m.group(2).splitlines()
+    return found
+
+
+def mode_problems(lines):
+    """Conversions of one function that the intermediate code does not hold to
+    their side of the MODE writes: (8-bit windows, problems)."""
+    defs, uses, where = {}, {}, {}
+    windows, problems, window, block = 0, [], 0, 0
+    for n, line in enumerate(lines):
+        if re.match(r"\S+:", line):
+            block += 1
+        m = re.match(r"\s*(%\S+) = ", line)
+        if m:
+            defs[m.group(1)] = n
+        for v in re.findall(r"%[\w.]+", line.split(" = ", 1)[-1]):
+            uses.setdefault(v, []).append(n)
+        if "llvm.amdgcn.s.setreg" in line and line.lstrip().split()[0] != "declare":
+            window = n if re.search(r"i32 1\)", line) else 0
+            windows += bool(window)
+        where[n] = (block, window)
+
+    def held(v):
+        """Whether v comes out of volatile asm: the line of that asm."""
+        n = defs.get(v)
+        while n is not None:
+            line = lines[n]
+            if "asm sideeffect" in line:
+                return n
+            m = re.search(r"= (?:extractvalue|bitcast|insertelement|extractelement|shufflevector)(.*)", line)
+            if not m:
+                return None
+            inner = re.findall(r"%[\w.]+", m.group(1))
+            n = defs.get(inner[-1]) if inner else None
+        return None
+
+    def goes_to(v, allowed):
+        """Whether every use of v is volatile asm or an `allowed` line."""
+        for n in uses.get(v, []):
+            if "asm sideeffect" in lines[n] or any(a in lines[n] for a in allowed):
+                continue
+            m = re.match(r"\s*(%\S+) = (bitcast|insertelement|extractelement|shufflevector)", lines[n])
+            if not m or not goes_to(m.group(1), allowed):
+                return False
+        return True
+
+    for n, line in enumerate(lines):
+        eight = any(c in line for c in CVT8)
+        if not eight and " to <2 x bfloat>" not in line:
+            continue
+        v = re.match(r"\s*(%\S+) = ", line).group(1)
+        if eight:
+            sources = re.findall(r"float (?:noundef )?(%[\w.]+)", line)[:2]
+        else:
+            sources = re.findall(r"<2 x float> (%[\w.]+)", line)
+        for s in sources:
+            at = held(s)
+            if at is None or where[at] != where[n] or bool(where[n][1]) != eight:
+                problems.append("operand: " + line.strip())
+        if not goes_to(v, CVT8 if eight else ()):
+            problems.append("result: " + line.strip())
+    return windows, problems
+
+
+def test_conversions_are_tied_to_the_mode_register(tmp_path):
+    ir = compiled(os.path.join(B.CSRC, "mxblock.hip"), str(tmp_path / "block.ll"), "-emit-llvm")
+    seen = 0
+    for name, lines in functions(ir).items():
+        windows, problems = mode_problems(lines)
+        if windows:
+            seen += 1
+            assert not problems, (name, problems[:4])
+    assert seen >= 16                       # norm and gated activation, two types, two 8-bit formats
+
+
+def test_conversions_come_out_in_their_window(tmp_path):
+    asm = compiled(os.path.join(B.CSRC, "mxblock.hip"), str(tmp_path / "block.s"))
+    eight = wide = 0
+    for kernel in re.split(r"\n\t\.globl\t", asm)[1:]:
+        on = False
+        if "s_setreg" not in kernel:
+            continue
+        for line in kernel.splitlines():
+            if re.match(r"\.?\w+:", line) or re.match(r"\ts_c?branch", line):
+                assert not on, kernel[:80]            # a window lies within a block
+            m = re.match(r"\ts_setreg_imm32_b32 hwreg\(HW_REG_MODE, 23, 1\), (\d)", line)
+            if m:
+                assert on != (m.group(1) == "1"), kernel[:80]
+                on = m.group(1) == "1"
+            if re.search(r"\tv_cvt_scalef32_pk_(fp8|bf8)_f32", line):
+                eight += 1
+                assert on, kernel[:80]
+            if "v_cvt_pk_bf16_f32" in line:
+                wide += 1
+                assert not on, kernel[:80]
+        assert not on
+    assert eight >= 64 and wide >= 64, (eight, wide)

@@ -172,7 +172,10 @@ constexpr int part_of(int n, int most)
 // The residual is read ahead, up to 8 or 16 units a lane: all bands' before
 // the first is staged, or a band's first part before its activation and each
 // further part before its stores, so its latency is met seldom; one load per
-// store and wait for it cost 10 us on 293 x 3443 x 2688.  (C may be the
+// store and wait for it cost 10 us on 293 x 3443 x 2688.  The band's LDS is the
+// wave's own, and the hardware keeps a wave's LDS accesses in order, so its
+// lanes hand values to each other without a barrier; the wave fences, which
+// cost no instruction, keep the compiler to that order.  (C may be the
 // residual: an element's only reader is the thread that stores it.)
 // 2048 x 8192 x 28672 E2M1 with bias, GELU and residual takes 245 us, the
 // product alone 232.
@@ -207,6 +210,7 @@ __device__ __forceinline__ void fused_rows(const Epilogue &ep, Stage stage_band,
     static_for<FM>([&](auto bc) {
         constexpr int b = decltype(bc)::value;
         stage_band(bc);
+        wave_fence();                        // staged by other lanes than read it
         if (!AHEAD && ep.residual) load(b, 0, res[0]);
         if (ep.act != ACT_NONE) {
             // in place, 16 values a lane and turn: enough independent chains
@@ -228,6 +232,7 @@ __device__ __forceinline__ void fused_rows(const Epilogue &ep, Stage stage_band,
                     *(v4f *)(stage + (t / QPR) * PITCH + (t % QPR) * 16) = v[u];
                 }
             }
+            wave_fence();                    // so are the activated values
         }
 #pragma unroll 1
         for (int first = 0; first < NIT; first += NB) {
@@ -259,6 +264,7 @@ __device__ __forceinline__ void fused_rows(const Epilogue &ep, Stage stage_band,
                 if (row + dr < M && col0 + lcol + dc < N) *(T *)(dst + (int64_t)dr * N + dc) = out[i];
             }
         }
+        wave_fence();                        // all lanes have read before the next band
     });
 }
 

@@ -1,11 +1,20 @@
-// mx_math.h -- gfx950 device arithmetic shared by the row operators and the
-// fused GEMM epilogue.
+// mx_math.h -- gfx950 device arithmetic and ordering shared by the row
+// operators, the expert routing and the fused GEMM epilogue.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 namespace mx {
+
+// Orders the wave's LDS accesses before this point against those after it,
+// across its lanes (the hardware keeps them in order; this keeps the compiler
+// to it).
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
 // Two BF16 values in one dword (low half: a), rounded to nearest even: one
 // v_cvt_pk_bf16_f32.

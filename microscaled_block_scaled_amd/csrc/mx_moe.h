@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "mx_math.h"
 #include "mx_rowops.h"
 
 namespace mx {
@@ -47,15 +48,6 @@ __device__ __forceinline__ uint64_t same_bin(int bin, bool live, int bits)
         m &= one ? v : ~v;
     }
     return m;
-}
-
-// Orders the wave's LDS accesses before this point against those after it,
-// across its lanes (the hardware keeps them in order; this keeps the compiler
-// to it).
-__device__ __forceinline__ void wave_fence()
-{
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
 }
 
 // Adds this wave's share of the workgroup's chunk, a run of chunk / 16

@@ -5,7 +5,11 @@ Conversions to 8-bit floats saturate while a bit of the MODE register is set,
 and BF16 conversions must not run while it is.  Both are pure to the compiler,
 so the source ties them to the register writes by empty volatile asm; that it
 does is read from the intermediate code, and that the instructions come out in
-that order from the assembly."""
+that order from the assembly.
+
+The fused epilogue hands values between a wave's lanes through LDS without a
+barrier; that every such hand-over crosses a wave fence is read from the
+intermediate code."""
 import os
 import re
 import subprocess
@@ -128,3 +132,90 @@ def test_conversions_come_out_in_their_window(tmp_path):
                 assert not on, kernel[:80]
         assert not on
     assert eight >= 64 and wide >= 64, (eight, wide)
+
+
+FUSED = """
+#include <hip/hip_runtime.h>
+#include "mx_epilogue.h"
+void use(const uint8_t *p, void *c, mx::Epilogue ep)
+{
+    hipLaunchKernelGGL((mx::tile_kernel<mx::FP8, mx::FP8, mx::OBF16, 128, 64, 2, 2, 3, mx::NoGroups,
+                                        mx::Epilogue>),
+                       dim3(1), dim3(256), 0, 0, p, p, p, p, c, 1, 1, 512, 1, 1, 4, 512, (int64_t)0,
+                       mx::NoGroups{}, ep);
+    hipLaunchKernelGGL((mx::tile_kernel<mx::FP8, mx::FP8, mx::OBF16, 128, 128, 2, 2, 3>),
+                       dim3(1), dim3(256), 0, 0, p, p, p, p, c, 1, 1, 512, 1, 1, 4, 512, (int64_t)0,
+                       mx::NoGroups{}, mx::NoEpilogue{});
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def fused_ir(tmp_path_factory):
+    """Intermediate code of a tile kernel with the fused epilogue (two bands a
+    wave) and of one without."""
+    at = tmp_path_factory.mktemp("fused")
+    (at / "fused.hip").write_text(FUSED)
+    return functions(compiled(str(at / "fused.hip"), str(at / "fused.ll"), "-emit-llvm", "-I", B.CSRC))
+
+
+def unfenced(lines):
+    """(staging stores, pairs of LDS accesses that different lanes' copies of
+    can meet without a wave fence between).  A band's sums are staged by
+    scalar stores; reads by other lanes follow, by way of an activation that
+    rewrites each value in the lane that read it; then the next band."""
+    blocks, name = {None: []}, None
+    for line in lines:
+        m = re.match(r"(\S+):", line)
+        if m:
+            name = m.group(1)
+            blocks[name] = []
+        else:
+            blocks[name].append(line)
+    text = {b: "\n".join(ls) for b, ls in blocks.items()}
+    nexts = {b: re.findall(r"label %(\S+?)(?:[,\s\]]|$)", t) for b, t in text.items()}
+
+    def access(line):
+        if "addrspace(3)" not in line or " = getelementptr" in line:
+            return None
+        if re.search(r"\bstore float\b.*ptr addrspace\(3\)", line):
+            return "stage"
+        if re.search(r"\bstore .*ptr addrspace\(3\)", line):
+            return "store"
+        if re.search(r"= load .*ptr addrspace\(3\)", line):
+            return "load"
+        return None
+
+    def reach(block, at):
+        """The LDS accesses after line `at` of a block up to a fence."""
+        found, seen, todo = set(), set(), [(block, at + 1)]
+        while todo:
+            b, i = todo.pop()
+            if (b, i) in seen:
+                continue
+            seen.add((b, i))
+            for n in range(i, len(blocks[b])):
+                if 'fence syncscope("wavefront")' in blocks[b][n] or "s_barrier" in blocks[b][n]:
+                    break
+                if access(blocks[b][n]):
+                    found.add((b, n))
+            else:
+                todo += [(x, 0) for x in nexts[b]]
+        return found
+
+    kind = {(b, n): access(line) for b, ls in blocks.items() for n, line in enumerate(ls) if access(line)}
+    to = {p: reach(*p) for p in kind}
+    staged = [p for p, k in kind.items() if k == "stage"]
+    bad = [(p, q) for p in staged for q in to[p] if kind[q] == "load"]
+    # after an activation's own rewrite only its own turn's reads may follow
+    bad += [(p, q) for p, k in kind.items() if k == "store" for q in to[p]
+            if kind[q] == "load" and p not in to[q]]
+    bad += [(p, q) for p in kind if kind[p] == "load" for q in to[p] if kind[q] == "stage"]
+    return len(staged), bad
+
+
+def test_staged_sums_are_fenced_between_lanes(fused_ir):
+    (lines,) = [ls for n, ls in fused_ir.items() if "Epilogue" in n and "NoEpilogue" not in n]
+    staged, bad = unfenced(lines)
+    assert staged >= 64
+    assert not bad, (len(bad), bad[:4])

@@ -19,6 +19,7 @@ enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4
 
 struct Epilogue {
     static constexpr bool fused = true, stream_b = false, order_all = true;
+    typedef void *C_ptr;
     const void *bias;            // N values, null: none
     const void *residual;        // rows of the output's type, pitch ldr, null: none
     int64_t ldr;

@@ -252,12 +252,16 @@ struct NoGroups {
 // tiles read B with the nontemporal hint.
 // order_all: workgroups are ordered per XCD also when their number is no
 // multiple of 8.
+// C_ptr: the kernel's C, which nothing else in it addresses unless C may be
+// the epilogue's residual.
 struct NoEpilogue {
     static constexpr bool fused = false, stream_b = true, order_all = false;
+    typedef void *__restrict__ C_ptr;
 };
 // The split-K slices of the fused GEMMs.
 struct PlainSums {
     static constexpr bool fused = false, stream_b = false, order_all = true;
+    typedef void *__restrict__ C_ptr;
 };
 template <typename EP> __device__ float bias_at(const EP &ep, int n);
 template <int OUT, typename EP>
@@ -313,7 +317,7 @@ template <int FA, int FB, int OUT, int BM, int BN, int WGM, int WGN, int S, type
 __global__ void __launch_bounds__(WGM * WGN * 64)
 tile_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
             const uint8_t *__restrict__ B, const uint8_t *__restrict__ Bs,
-            void *__restrict__ C, int M, int N, int K, int tiles_m, int tiles_n, int gm,
+            typename EP::C_ptr C, int M, int N, int K, int tiles_m, int tiles_n, int gm,
             int kchunk, int64_t cplane, GT groups = GT{}, EP ep = EP{})
 {
     constexpr int NW = WGM * WGN;

@@ -34,9 +34,13 @@ def compiled(source, out, *more):
 def functions(ir):
     """{name: lines} of the kernels of intermediate code."""
     found = {}
-    for m in re.finditer(r"^define [^\n]*@(\S+?)\([^\n]*\{\n(.*?)^\}", ir, re.M | re.S):
-        found[m.group(1)] = m.group(2).splitlines()
+    for m in re.finditer(r"^define [^\n]*@(\S+?)\(([^\n]*)\{\n(.*?)^\}", ir, re.M | re.S):
+        found[m.group(1)] = m.group(3).splitlines()
+        parameters[m.group(1)] = re.split(r", (?=ptr|i\d|%)", m.group(2))
     return found
+
+
+parameters = {}                         # of the functions found: text of each
 
 
 def mode_problems(lines):
@@ -219,3 +223,12 @@ def test_staged_sums_are_fenced_between_lanes(fused_ir):
     staged, bad = unfenced(lines)
     assert staged >= 64
     assert not bad, (len(bad), bad[:4])
+
+
+def test_c_may_be_the_residual(fused_ir):
+    """The compiler is told that nothing else addresses C in the kernels
+    without an epilogue, and is not told so where C may be the residual."""
+    told = {"noalias" in parameters[n][4] for n in fused_ir if "NoEpilogue" in n}
+    assert told == {True}
+    told = {"noalias" in parameters[n][4] for n in fused_ir if "NoEpilogue" not in n and "Epilogue" in n}
+    assert told == {False}

@@ -210,6 +210,22 @@ __device__ __forceinline__ float block_sum(float v, float *part)
     return t;
 }
 
+// 1 / sqrt(x) for x >= 0, rounded once: the hardware's root r and one Newton
+// step r + r / 2 (1 - x r^2), whose residual is formed to twice FP32's width
+// by two fused products.  (1 / sqrtf rounds twice, an error that a whole row
+// of the norm shares.)  The hardware's root takes no subnormals, so small x is
+// scaled by a square; 0 and infinity keep its infinity and 0.
+__device__ __forceinline__ float root_reciprocal(float x)
+{
+    const bool small = x < 0x1p-100f;
+    const float s = small ? x * 0x1p64f : x;
+    const float r = __builtin_amdgcn_rsqf(s);
+    const float h = s * r, l = fmaf(s, r, -h);             // h + l = s r
+    const float e = fmaf(-l, r, fmaf(-h, r, 1.f));         // 1 - s r^2
+    const float y = s > 0.f && s < __builtin_inff() ? fmaf(0.5f * r, e, r) : r;
+    return small ? y * 0x1p32f : y;
+}
+
 // 8 weights as loaded, FP32 or BF16 by a uniform flag.
 __device__ __forceinline__ raw8<IN_F32> load_weight(const void *w, int col, int bf16)
 {
@@ -283,7 +299,7 @@ norm_quantize(NormArgs a)
             for (int i = 0; i < 8; ++i) sum = fmaf(h[i], h[i], sum);
         }
         sum = block_sum(sum, part[flip]);
-        const float rstd = 1.f / sqrtf(sum / (float)a.width + a.eps);
+        const float rstd = root_reciprocal(sum / (float)a.width + a.eps);
         if (a.rstd && tid == 0) a.rstd[row] = rstd;
 #pragma unroll
         for (int c = 0; c < C; ++c) {

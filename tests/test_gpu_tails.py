@@ -1,4 +1,7 @@
-"""GPU tests of the arithmetic's far ends."""
+"""GPU tests of the arithmetic's far ends.
+
+Tolerances: rstd with an exact mean and eps 0 has only its own rounding, half
+a unit in the last place; the correction's own error is below 2^-20 of one."""
 import numpy as np
 import pytest
 
@@ -19,6 +22,25 @@ def _dev(a, dtype="float32"):
 
 def _h64(t):
     return t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype,top", [("float32", 64), ("bfloat16", 16)])
+@pytest.mark.parametrize("width", [32, 1024, 8192, 32768])
+def test_rstd_is_rounded_once(width, dtype, top):
+    """Integers whose squares' sum is exact in any order: rstd is 1 / sqrt of
+    an exact mean."""
+    log("rstd of exact means, width %d %s" % (width, dtype))
+    rng = np.random.default_rng(width + top)
+    most = min(top, int((2.0 ** 24 / width) ** 0.5))
+    x = rng.integers(-most, most + 1, (400, width)).astype(np.float64)
+    x *= 2.0 ** rng.integers(-50, 50, (400, 1))            # exact too
+    x[:3] = [[2.0 ** -70], [2.0 ** 55], [1.0]]
+    o = mxg.mx_rmsnorm_quantize(_dev(x, dtype), _dev(np.ones(width)), mxg.FMT_E4M3, eps=0.0,
+                                need_rstd=True)
+    got = o.rstd.cpu().numpy()
+    want = 1.0 / np.sqrt((x * x).mean(1))
+    assert (abs(got - want) <= 0.501 * np.spacing(got).astype(np.float64)).all(), \
+        float((abs(got - want) / np.spacing(got)).max())
 
 
 @pytest.mark.parametrize("fmt", [mxg.FMT_E4M3, mxg.FMT_E5M2, mxg.FMT_E2M1])

@@ -521,7 +521,9 @@ int mx_rmsnorm_backward(int dtype, int w_dtype, int64_t rows, int64_t width, con
  * Gated activation and MX quantization: GU holds rows of 2 * width values,
  * gate then up (the output of a fused gate/up product), and
  *   (Q, Q_scale) = MX(gate * sigmoid(gate) * up).
- * width as for mx_rmsnorm_quantize; ld >= 2 * width.
+ * width as for mx_rmsnorm_quantize; ld >= 2 * width.  The sigmoid keeps its
+ * precision down to 2^-252, so that a far negative gate and a large up give
+ * their product; below that it is 0.
  */
 int mx_swiglu_quantize(int fmt, int dtype, int64_t rows, int64_t width, const void *GU,
                        int64_t ld, void *Q, void *Q_scale, void *stream);
@@ -597,7 +599,7 @@ int mx_moe_combine_backward(int dtype, int64_t tokens, int64_t top, int64_t widt
                             void *dY, float *dweights, void *stream);
 
 /* Activations of a fused epilogue: none, max(x, 0), x * sigmoid(x), and GELU
- * by erf or by its tanh form. */
+ * by erf or by its tanh form (sigmoids as for mx_swiglu_quantize). */
 enum { MX_ACT_NONE = 0, MX_ACT_RELU = 1, MX_ACT_SILU = 2, MX_ACT_GELU = 3, MX_ACT_GELU_TANH = 4 };
 
 /*

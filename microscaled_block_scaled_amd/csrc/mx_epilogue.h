@@ -46,6 +46,13 @@ __device__ __forceinline__ float normal_tail(float a)
     return s * t * __builtin_amdgcn_exp2f(a * a * -0.721347520f);      // -log2(e) / 2
 }
 
+// 2 sqrt(2 / pi) (v + 0.044715 v^3)
+__device__ __forceinline__ float tanh_argument(float v)
+{
+    return 1.59576912f * v * fmaf(0.044715f * v, v, 1.f);
+}
+
+// An activation for values that are not in the tail.
 template <int ACT>
 __device__ __forceinline__ float act_of(float v)
 {
@@ -55,21 +62,39 @@ __device__ __forceinline__ float act_of(float v)
         const float q = normal_tail(fabsf(v));
         return v * (v > 0.f ? 1.f - q : q);
     }
-    // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), u = sqrt(2/pi) (v + 0.044715 v^3)
-    if constexpr (ACT == ACT_GELU_TANH)
-        return v * sigmoid(1.59576912f * v * fmaf(0.044715f * v, v, 1.f));
+    // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u))
+    if constexpr (ACT == ACT_GELU_TANH) return v * sigmoid(tanh_argument(v));
     return v;
+}
+
+// And for any value.
+template <int ACT>
+__device__ __forceinline__ float act_any(float v)
+{
+    if constexpr (ACT == ACT_SILU || ACT == ACT_GELU_TANH) {
+        const float w = ACT == ACT_SILU ? v : tanh_argument(v);
+        if (w < kSigmoidTail) return v * sigmoid_tail(w) * kTailScale;
+    }
+    return act_of<ACT>(v);
 }
 
 __device__ __forceinline__ float act_apply(float v, int act)
 {
     switch (act) {
-    case ACT_RELU: return act_of<ACT_RELU>(v);
-    case ACT_SILU: return act_of<ACT_SILU>(v);
-    case ACT_GELU: return act_of<ACT_GELU>(v);
-    case ACT_GELU_TANH: return act_of<ACT_GELU_TANH>(v);
+    case ACT_RELU: return act_any<ACT_RELU>(v);
+    case ACT_SILU: return act_any<ACT_SILU>(v);
+    case ACT_GELU: return act_any<ACT_GELU>(v);
+    case ACT_GELU_TANH: return act_any<ACT_GELU_TANH>(v);
     default: return v;
     }
+}
+
+// The values below which the activation's sigmoid is in its tail: by the
+// argument itself, or by the cubic, which is -85.0 at -9.9 (and -87.3 at
+// -10.0); no values for the others.
+__device__ __forceinline__ float act_tail(int act)
+{
+    return act == ACT_SILU ? kSigmoidTail : act == ACT_GELU_TANH ? -9.9f : -__builtin_inff();
 }
 
 template <int ACT>
@@ -218,6 +243,7 @@ __device__ __forceinline__ void fused_rows(const Epilogue &ep, Stage stage_band,
             // to keep the wave busy, one copy of the code per band
             constexpr int QPR = WTN / 4;                        // float4 per row
             static_assert(QPR % 8 == 0, "whole turns");
+            const float tail = act_tail(ep.act);
 #pragma unroll 1
             for (int t0 = lane; t0 < 32 * QPR; t0 += 256) {
                 v4f v[4];
@@ -225,6 +251,17 @@ __device__ __forceinline__ void fused_rows(const Epilogue &ep, Stage stage_band,
                 for (int u = 0; u < 4; ++u) {
                     const int t = t0 + u * 64;
                     v[u] = *(const v4f *)(stage + (t / QPR) * PITCH + (t % QPR) * 16);
+                }
+                float all[16];
+                __builtin_memcpy(all, v, sizeof(all));
+                if (any_below(all, tail)) {          // seldom: value by value, in little code
+#pragma unroll 1
+                    for (int e = 0; e < 16; ++e) {
+                        const int t = t0 + (e >> 2) * 64;
+                        float *x = (float *)(stage + (t / QPR) * PITCH + (t % QPR) * 16) + (e & 3);
+                        *x = act_apply(*x, ep.act);
+                    }
+                    continue;
                 }
                 act_apply16(v, ep.act);
 #pragma unroll

@@ -143,7 +143,7 @@ FUSED = """
 #include "mx_epilogue.h"
 void use(const uint8_t *p, void *c, mx::Epilogue ep)
 {
-    hipLaunchKernelGGL((mx::tile_kernel<mx::FP8, mx::FP8, mx::OBF16, 128, 64, 2, 2, 3, mx::NoGroups,
+    hipLaunchKernelGGL((mx::tile_kernel<mx::FP8, mx::FP8, mx::OBF16, 128, 128, 2, 2, 3, mx::NoGroups,
                                         mx::Epilogue>),
                        dim3(1), dim3(256), 0, 0, p, p, p, p, c, 1, 1, 512, 1, 1, 4, 512, (int64_t)0,
                        mx::NoGroups{}, ep);
@@ -156,18 +156,18 @@ void use(const uint8_t *p, void *c, mx::Epilogue ep)
 
 @pytest.fixture(scope="module")
 def fused_ir(tmp_path_factory):
-    """Intermediate code of a tile kernel with the fused epilogue (two bands a
-    wave) and of one without."""
+    """Intermediate code of a tile kernel with the fused epilogue (two bands and
+    two activation turns a wave) and of one without."""
     at = tmp_path_factory.mktemp("fused")
     (at / "fused.hip").write_text(FUSED)
-    return functions(compiled(str(at / "fused.hip"), str(at / "fused.ll"), "-emit-llvm", "-I", B.CSRC))
+    return functions(compiled(str(at / "fused.hip"), str(at / "fused.ll"), "-emit-llvm"))
 
 
 def unfenced(lines):
-    """(staging stores, pairs of LDS accesses that different lanes' copies of
-    can meet without a wave fence between).  A band's sums are staged by
-    scalar stores; reads by other lanes follow, by way of an activation that
-    rewrites each value in the lane that read it; then the next band."""
+    """(LDS stores, pairs of LDS accesses that different lanes' copies of can
+    meet without a wave fence between).  A band's sums are staged; reads by
+    other lanes follow, by way of an activation that rewrites each value in the
+    lane that read it; then the next band."""
     blocks, name = {None: []}, None
     for line in lines:
         m = re.match(r"(\S+):", line)
@@ -182,8 +182,6 @@ def unfenced(lines):
     def access(line):
         if "addrspace(3)" not in line or " = getelementptr" in line:
             return None
-        if re.search(r"\bstore float\b.*ptr addrspace\(3\)", line):
-            return "stage"
         if re.search(r"\bstore .*ptr addrspace\(3\)", line):
             return "store"
         if re.search(r"= load .*ptr addrspace\(3\)", line):
@@ -209,19 +207,15 @@ def unfenced(lines):
 
     kind = {(b, n): access(line) for b, ls in blocks.items() for n, line in enumerate(ls) if access(line)}
     to = {p: reach(*p) for p in kind}
-    staged = [p for p, k in kind.items() if k == "stage"]
-    bad = [(p, q) for p in staged for q in to[p] if kind[q] == "load"]
-    # after an activation's own rewrite only its own turn's reads may follow
-    bad += [(p, q) for p, k in kind.items() if k == "store" for q in to[p]
-            if kind[q] == "load" and p not in to[q]]
-    bad += [(p, q) for p in kind if kind[p] == "load" for q in to[p] if kind[q] == "stage"]
-    return len(staged), bad
+    # a value's own rewriting in a loop reaches back to where it was read
+    bad = [(p, q) for p in kind for q in to[p] if {kind[p], kind[q]} == {"load", "store"} and p not in to[q]]
+    return sum(k == "store" for k in kind.values()), bad
 
 
 def test_staged_sums_are_fenced_between_lanes(fused_ir):
     (lines,) = [ls for n, ls in fused_ir.items() if "Epilogue" in n and "NoEpilogue" not in n]
-    staged, bad = unfenced(lines)
-    assert staged >= 64
+    stores, bad = unfenced(lines)
+    assert stores >= 64
     assert not bad, (len(bad), bad[:4])
 
 

@@ -142,6 +142,9 @@ void fused_plan(int fmt_a, int fmt_b, int64_t M, int64_t N, int64_t K, int max_s
             double t = (double)cdiv(tiles * split, kCUs) * c.cost * unit *
                        (double)(split > 1 ? k : K) / 128.0;
             if (split > 1) t += 3.5 + 2.3e-6 * (double)(M * N * split);
+            // a launch has less than 2^32 threads, and 2^24 tiles of 64 columns
+            // (N = 2^30) have that many: such a grid only where all are
+            if (tiles * split * c.wgm * c.wgn * 64 >= (int64_t)1 << 32) t *= 1e9;
             if (best >= 0.0 && t >= best) continue;
             best = t;
             p->variant = MX_VARIANT_TILE;

@@ -97,14 +97,16 @@ __device__ __forceinline__ void saturate_fp8(bool on)
 }
 
 // To the compiler a conversion is pure: nothing in it says that it depends on
-// MODE, so nothing keeps it on its side of saturate_fp8.  Its operands and its
-// result pass through empty volatile asm, which costs no instruction and
-// stays in order with the register writes: what is computed from a held value
-// comes after, what is held was computed before.
-__device__ __forceinline__ void hold(float (&v)[8])
+// MODE, so nothing keeps it on its side of saturate_fp8.  One of its operands
+// and its result pass through empty volatile asm, which costs no instruction
+// and stays in order with the register writes: what is computed from a held
+// value comes after, what is held was computed before.  (The 8-bit conversions
+// hold their scale: holding the values took registers, and 6 % of a norm of
+// FP32 rows of 32768 that is short of them.)
+template <typename T>
+__device__ __forceinline__ void hold(T &v)
 {
-    asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]),
-                      "+v"(v[6]), "+v"(v[7]));
+    asm volatile("" : "+v"(v));
 }
 
 // pack8 in a kernel that also converts to format F: outside of the windows
@@ -113,9 +115,11 @@ template <int IN, int F>
 __device__ __forceinline__ raw8<IN> pack8_beside(float (&v)[8])
 {
     constexpr bool HELD = IN == IN_BF16 && (F == FP8 || F == BF8);
-    if constexpr (HELD) hold(v);
+    if constexpr (HELD)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) hold(v[i]);
     raw8<IN> r = pack8<IN>(v);
-    if constexpr (HELD) asm volatile("" : "+v"(r.q[0]));
+    if constexpr (HELD) hold(r.q[0]);
     return r;
 }
 
@@ -164,22 +168,21 @@ __device__ __forceinline__ void quantize8(const float (&v)[8], uint8_t *q, uint8
     } else {
         typedef short s16x2 __attribute__((vector_size(4)));
         s16x2 w[2] = {};
-        float u[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = v[i];
+        float by = scale;
         saturate_fp8(true);
-        hold(u);
+        hold(by);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if constexpr (F == BF8) {
-                w[i] = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w[i], u[4 * i], u[4 * i + 1], scale, false);
-                w[i] = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w[i], u[4 * i + 2], u[4 * i + 3], scale, true);
+                w[i] = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w[i], v[4 * i], v[4 * i + 1], by, false);
+                w[i] = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w[i], v[4 * i + 2], v[4 * i + 3], by, true);
             } else {
-                w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w[i], u[4 * i], u[4 * i + 1], scale, false);
-                w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w[i], u[4 * i + 2], u[4 * i + 3], scale, true);
+                w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w[i], v[4 * i], v[4 * i + 1], by, false);
+                w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w[i], v[4 * i + 2], v[4 * i + 3], by, true);
             }
         }
-        asm volatile("" : "+v"(w[0]), "+v"(w[1]));
+        hold(w[0]);
+        hold(w[1]);
         saturate_fp8(false);
         const uint64_t both = (uint64_t)__builtin_bit_cast(uint32_t, w[0]) |
                               ((uint64_t)__builtin_bit_cast(uint32_t, w[1]) << 32);

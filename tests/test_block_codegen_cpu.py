@@ -64,16 +64,12 @@ def mode_problems(lines):
     def held(v):
         """Whether v comes out of volatile asm: the line of that asm."""
         n = defs.get(v)
-        while n is not None:
-            line = lines[n]
-            if "asm sideeffect" in line:
-                return n
-            m = re.search(r"= (?:extractvalue|bitcast|insertelement|extractelement|shufflevector)(.*)", line)
-            if not m:
-                return None
-            inner = re.findall(r"%[\w.]+", m.group(1))
-            n = defs.get(inner[-1]) if inner else None
-        return None
+        if n is None or "asm sideeffect" in lines[n]:
+            return n
+        m = re.search(r"= (?:extractvalue|bitcast|insertelement|extractelement|shufflevector)(.*)",
+                      lines[n])
+        inner = [held(x) for x in re.findall(r"%[\w.]+", m.group(1))] if m else []
+        return next((at for at in inner if at is not None), None)
 
     def goes_to(v, allowed):
         """Whether every use of v is volatile asm or an `allowed` line."""
@@ -91,13 +87,12 @@ def mode_problems(lines):
             continue
         v = re.match(r"\s*(%\S+) = ", line).group(1)
         if eight:
-            sources = re.findall(r"float (?:noundef )?(%[\w.]+)", line)[:2]
+            s = re.findall(r"float (?:noundef )?(%[\w.]+)", line)[2]      # the scale
         else:
-            sources = re.findall(r"<2 x float> (%[\w.]+)", line)
-        for s in sources:
-            at = held(s)
-            if at is None or where[at] != where[n] or bool(where[n][1]) != eight:
-                problems.append("operand: " + line.strip())
+            s = re.search(r"<2 x float> (%[\w.]+)", line).group(1)
+        at = held(s)
+        if at is None or where[at] != where[n] or bool(where[n][1]) != eight:
+            problems.append("operand: " + line.strip())
         if not goes_to(v, CVT8 if eight else ()):
             problems.append("result: " + line.strip())
     return windows, problems

@@ -97,6 +97,22 @@ def test_gated_activation_gradient_in_the_tail(dtype):
     assert (abs(got[:, :len(g)]) > 2.0 ** -120).all()       # d_gate is far from underflow
 
 
+def test_gated_activation_gradient_in_place():
+    """dGU may be GU itself, also where a wave writes its values twice."""
+    import torch
+    log("gated activation's gradient in place")
+    g, up = _tail()
+    gu = _dev(np.concatenate([g, up])[None].repeat(3, 0))
+    gu[1:, 3::5] = 0.25
+    dy = _dev(np.random.default_rng(3).random((3, len(g))))
+    want = mxg.mx_swiglu_backward(dy, gu)
+    rc = mxg.lib().mx_swiglu_backward(mxg.IN_FP32, 3, len(g), dy.data_ptr(), len(g), gu.data_ptr(),
+                                      2 * len(g), gu.data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream or None)
+    torch.cuda.synchronize()
+    assert rc == mxg.MX_OK and torch.equal(gu, want)
+
+
 @pytest.mark.parametrize("M", [3, 70])
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 def test_epilogue_in_the_tail(act, M):

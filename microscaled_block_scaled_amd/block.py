@@ -5,7 +5,9 @@ and products with a fused epilogue (include/mxgemm.h).
 Like the rest of the binding it only marshals arguments; every result is
 computed by the library's HIP kernels, on the current stream or on ``stream``
 (a raw stream handle).  Outputs and workspaces of a call on another stream
-than the current one are allocated for that stream.
+than the current one are allocated for that stream.  Results carry no autograd
+history, whatever their inputs carry: the backward functions are called by
+name, as examples/moe_block.py does.
 
 A call with plain tensors on the current device and stream is checked and
 launched in one step by the compiled module _native (csrc/binding.cpp), which

@@ -23,7 +23,10 @@
 // partial tiles are added, so a workgroup with several groups does not
 // refill its pipeline from empty for each.  Every wait for memory is the one explicit
 // wait per slab: no load writes a register, so the compiler has nothing of
-// its own to wait for.  Rows of A past M and of B past N lie past the copy
+// its own to wait for.  (The fused epilogue's bias and residual do: loads
+// return in order, so waiting for them waits for every copy issued before
+// them, and a workgroup with several groups refills its rings after each.)
+// Rows of A past M and of B past N lie past the copy
 // descriptor's num_records and are not fetched (their results are never
 // stored).  B is read once and carries the nontemporal hint.
 #pragma once
@@ -316,7 +319,8 @@ decode_body(const uint8_t *__restrict__ A, const uint8_t *__restrict__ As,
     // In the MFMA result lane (c, g) holds, in element e, row
     // 8(e/4) + 4g + e%4 of column c; element e of lane l is kept at float
     // 64 e + l of the slot.  The barriers order LDS only: the stream's copies
-    // into the rings stay in flight.
+    // into the rings stay in flight, unless the epilogue loads a bias or a
+    // residual.
     auto add_and_store = [&](int gi) {
         const int n0 = group_n0(gi), rows_b = min(kDecodeRows, N - n0);
         const int at_slot = wave * G::WAVE_LDS + (rslot == 0 ? S - 1 : rslot - 1) * SLOT;

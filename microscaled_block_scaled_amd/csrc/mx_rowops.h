@@ -261,8 +261,11 @@ struct NormArgs {
 //
 // One workgroup per row, the row in registers (C chunks of 8 per thread,
 // chunk c of thread t holding values 8 (c T + t) .., T threads), so the row is
-// read once for both the sum and the norm.  The weights are loaded before the
-// sum is known, beside the row itself.  Bound by HBM: 16384 x 8192 BF16 to
+// read once for both the sum and the norm.  Beyond 16384 values (FP32) or
+// 32768 the 128 registers of 1024 threads do not hold all of it and some are
+// spilled: 1024 x 32768 FP32 112 us, 3.9 TB/s of what it must move, 1024 x
+// 65536 BF16 182 us, 2.6 TB/s.  The weights are loaded before the sum is known,
+// beside the row itself.  Bound by HBM: 16384 x 8192 BF16 to
 // E4M3 with residual 157 us a call, 6.0 TB/s of what it must move.
 template <int IN, int F, int MAXT, int C>
 __global__ void __launch_bounds__(MAXT)
@@ -339,7 +342,10 @@ struct NormGradArgs {
 // weights and dw sums in registers over all of them.  The next row's loads
 // are issued before the current row's sum is joined over the workgroup, so
 // memory stays busy across the barrier.  4001 x 5120 BF16: 31 us, 5.5 TB/s of
-// HBM, and 5 us for column_sum.
+// HBM, and 5 us for column_sum.  Beyond 8192 values a thread has 4 or 8 chunks
+// and its dw sums, weights and two rows pass the registers: with the spills
+// 2048 x 16384 takes 66 us in BF16 and 250 in FP32 (4096 x 8192, the same
+// bytes, 52 and 105), 512 x 65536 BF16 443.
 template <int IN, int MAXT, int C>
 __global__ void __launch_bounds__(MAXT)
 norm_grad(NormGradArgs a)

@@ -67,7 +67,7 @@ void with_fmt(int dtype, int fmt, Fn f)
 // Calls f(MAXT, C, threads): chunks of 8 values per thread, the threads of a
 // row's workgroup, and the most threads of that kernel.  Rows of up to 8192
 // values take FIRST chunks per thread; longer rows what 512 or 1024 threads
-// need.
+// need, with registers spilled as the kernels say.
 template <int FIRST, typename Fn>
 void with_row(int64_t width, Fn f)
 {

@@ -266,7 +266,7 @@ struct NormArgs {
 // spilled: 1024 x 32768 FP32 112 us, 3.9 TB/s of what it must move, 1024 x
 // 65536 BF16 182 us, 2.6 TB/s.  The weights are loaded before the sum is known,
 // beside the row itself.  Bound by HBM: 16384 x 8192 BF16 to
-// E4M3 with residual 157 us a call, 6.0 TB/s of what it must move.
+// E4M3 with residual 156 us a call, 6.0 TB/s of what it must move.
 template <int IN, int F, int MAXT, int C>
 __global__ void __launch_bounds__(MAXT)
 norm_quantize(NormArgs a)
@@ -522,9 +522,10 @@ column_sum(const float *__restrict__ part, float *__restrict__ dw, int n, int wi
 // y = silu(gate) * up -> MX, gate and up the two halves of a row of 2 * width
 // values.  A thread takes one chunk of columns (workgroup x of the row) in
 // the rows blockIdx.y, blockIdx.y + gridDim.y, ...  A wave with a gate in the
-// sigmoid's tail writes its chunks again with those values; a branch ahead of
-// the stores instead took 5 % of an FP32 gradient.  Bound by HBM: 2048 x 28672
-// BF16 to E4M3 50 us a call, 6.0 TB/s, with 19 VALU instructions a value.
+// sigmoid's tail writes its chunks again with those values (an FP32 gradient of
+// 999 x 25600 took 95.5 us so, 97 with the choice ahead of its stores, 100 with
+// stores on both sides of it).  Bound by HBM: 2048 x 28672
+// BF16 to E4M3 50 us a call, 5.9 TB/s, with 20 VALU instructions a value.
 struct GluArgs {
     const void *gu;
     uint8_t *q, *s;
